@@ -13,4 +13,6 @@ from ._binding import (  # noqa: F401
     attn_kernel_launches, attn_debug_wait_timeout, attn_debug_unit_rates, attn_debug_unit_schedule, library_path,
     load_library,
     exported_symbols, attn_bwd, attn_bwd_ptr, attn_bwd_workspace_size,
+    attn_paged_tables, attn_paged_tables_ptr, attn_paged_append, attn_paged_append_ptr, attn_paged_fwd,
+    attn_paged_fwd_ptr, attn_paged_fwd_workspace_size,
 )

@@ -26,7 +26,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_splitkv", "attn_fwd_splitkv_wor
             "attn_fwd_splitkv_noalloc", "attn_status_str", "attn_last_device_status",
             "attn_check_device_status",
             "attn_kernel_launches", "attn_debug_wait_timeout", "attn_bwd", "attn_bwd_workspace_size",
-            "attn_debug_unit_rates", "attn_debug_unit_schedule")
+            "attn_debug_unit_rates", "attn_debug_unit_schedule", "attn_paged_tables", "attn_paged_append",
+            "attn_paged_fwd", "attn_paged_fwd_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +93,16 @@ def load_library():
         lib.attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, ctypes.c_float, I, P,
                                  ctypes.c_size_t, P]
         lib.attn_bwd.restype = I
+        L = ctypes.c_longlong
+        lib.attn_paged_tables.argtypes = [P, P, I, I, P, I, P, P, I, L, P, P, P, I, P, P]
+        lib.attn_paged_tables.restype = I
+        lib.attn_paged_append.argtypes = [P, P, P, P, P, I, I, I, I, I, L, L, L, L, L, P]
+        lib.attn_paged_append.restype = I
+        lib.attn_paged_fwd_workspace_size.argtypes = [I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+        lib.attn_paged_fwd_workspace_size.restype = I
+        lib.attn_paged_fwd.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, L, L, L, L, L, I,
+                                       ctypes.c_float, I, P, ctypes.c_size_t, P]
+        lib.attn_paged_fwd.restype = I
         _lib = lib
         return lib
 
@@ -274,6 +285,217 @@ def attn_bwd(q, k, v, o, lse, do, causal: int = 0, scale: float | None = None, d
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd")
     return dq, dk, dv
+
+
+# ---- paged key/value cache
+
+def _paged_call(tensors, stream):
+    """(device, stream handle) of a call on `tensors`, which are all on one GPU.
+    A stream handle of another device's current stream is never taken."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != device or not t.is_cuda):
+            raise AttnError(ATTN_ERR_INVALID_ARG, "all tensors must be on one CUDA device")
+    if stream is None:
+        import torch
+        return device, torch.cuda.current_stream(device).cuda_stream
+    return device, _stream_handle(stream)
+
+
+class _on:
+    """Makes `device` current and, for a stream the caller passed, allocates on that
+    stream, so that memory freed after the call is reused in its order."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if torch.cuda.current_device() != device.index:
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            self.guards.append(torch.cuda.stream(s))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _need(name, t, dtype, shape=None):
+    if t.dtype != dtype or (shape is not None and tuple(t.shape) != shape) or not t.is_contiguous():
+        want = "" if shape is None else f" of shape {shape}"
+        raise AttnError(ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor{want}")
+
+
+def _check_table(table, n_seqs):
+    import torch
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seqs or table.stride(1) != 1:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "block_table must be int32 [n_seqs, max_pages] with contiguous rows")
+    return table.stride(0) if n_seqs > 1 else table.shape[1]
+
+
+def _check_cache(k_cache, v_cache):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or \
+            k_cache.dtype != v_cache.dtype or k_cache.stride(3) != 1:
+        raise AttnError(ATTN_ERR_INVALID_ARG,
+                        "k_cache and v_cache must be [n_pages, page_size, Hkv, D] of one type, shape and strides, "
+                        "D contiguous")
+
+
+def _row_stride(name, t, heads, D):
+    """Row stride of [T, heads, D] with contiguous heads (a slice of a wider row is fine)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != D):
+        raise AttnError(ATTN_ERR_INVALID_ARG, f"{name} must be [T, {heads}, {D}] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def attn_paged_tables_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return int(load_library().attn_paged_tables(*args))
+
+
+def attn_paged_append_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return int(load_library().attn_paged_append(*args))
+
+
+def attn_paged_fwd_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return int(load_library().attn_paged_fwd(*args))
+
+
+def attn_paged_tables(ctx_lens, new_lens, free_pages, block_table, page_size: int, max_tokens: int, free_head=None,
+                      cu_new=None, kv_lens=None, slot_map=None, counts=None, stream=None):
+    """The tables of one step, built on the GPU from the lengths of its sequences.
+
+    ctx_lens, new_lens: int32 [n_seqs], cached and new tokens of each sequence.
+    free_pages: int32 [n_free], taken in order from entry free_head (int32 [1]; None: 0).
+    block_table: int32 [n_seqs, max_pages], extended in place by the new tokens' pages.
+    Returns (cu_new int32 [n_seqs + 1], kv_lens int32 [n_seqs], slot_map int64
+    [max_tokens], counts int32 [4]: new tokens, next free_head, missing pages,
+    sequences longer than a table row).  Outputs are allocated here if None.
+    """
+    import torch
+    n = ctx_lens.shape[0]
+    device, handle = _paged_call((ctx_lens, new_lens, free_pages, block_table, free_head, cu_new, kv_lens, slot_map,
+                                  counts), stream)
+    i32 = torch.int32
+    _need("ctx_lens", ctx_lens, i32, (n,))
+    _need("new_lens", new_lens, i32, (n,))
+    _need("free_pages", free_pages, i32, (free_pages.numel(),))
+    if free_head is not None:
+        _need("free_head", free_head, i32, (1,))
+    table_stride = _check_table(block_table, n)
+    with _on(device, stream):
+        if cu_new is None:
+            cu_new = torch.empty(n + 1, dtype=i32, device=device)
+        if kv_lens is None:
+            kv_lens = torch.empty(n, dtype=i32, device=device)
+        if slot_map is None:
+            slot_map = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        if counts is None:
+            counts = torch.empty(4, dtype=i32, device=device)
+        _need("cu_new", cu_new, i32, (n + 1,))
+        _need("kv_lens", kv_lens, i32, (n,))
+        _need("slot_map", slot_map, torch.int64, (max_tokens,))
+        _need("counts", counts, i32, (4,))
+        st = attn_paged_tables_ptr(ctx_lens.data_ptr(), new_lens.data_ptr(), n, int(page_size), free_pages.data_ptr(),
+                                   free_pages.numel(), 0 if free_head is None else free_head.data_ptr(),
+                                   block_table.data_ptr(), block_table.shape[1], table_stride, cu_new.data_ptr(),
+                                   kv_lens.data_ptr(), slot_map.data_ptr(), int(max_tokens), counts.data_ptr(), handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_tables")
+    return cu_new, kv_lens, slot_map, counts
+
+
+def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
+    """Write the rows of k and v ([T, Hkv, D], heads contiguous, any row stride) into
+    slots slot_map[t] (int64 [T], rows outside the cache skipped) of k_cache and v_cache
+    ([n_pages, page_size, Hkv, D], any strides with D contiguous), in place."""
+    import torch
+    device, handle = _paged_call((k, v, slot_map, k_cache, v_cache), stream)
+    _check_cache(k_cache, v_cache)
+    n_pages, page_size, Hkv, D = k_cache.shape
+    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "k, v and the cache must be bf16 or float16, all one type")
+    _need("slot_map", slot_map, torch.int64, (k.shape[0],))
+    if v.shape[0] != k.shape[0]:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "k and v must have the same number of rows")
+    ks, vs = _row_stride("k", k, Hkv, D), _row_stride("v", v, Hkv, D)
+    ps, ts, hs, _ = k_cache.stride()
+    with _on(device, stream):
+        st = attn_paged_append_ptr(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+                                   v_cache.data_ptr(), k.shape[0], Hkv, D, n_pages, page_size, ks, vs, ps, ts, hs,
+                                   handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_append")
+
+
+def attn_paged_fwd_workspace_size(total_q: int, max_q_len: int, Hq: int, Hkv: int, D: int, page_size: int) -> int:
+    """Workspace bytes attn_paged_fwd needs on the current device (0: none)."""
+    n = ctypes.c_size_t(0)
+    st = int(load_library().attn_paged_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, ctypes.byref(n)))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_fwd_workspace_size")
+    return int(n.value)
+
+
+def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: int | None = None, causal: int = 1,
+                   scale: float | None = None, o=None, lse=None, workspace=None, stream=None, want_lse: bool = True):
+    """Attention of a ragged batch of new tokens over a paged cache.
+
+    q: bf16 or float16 [T, Hq, D], heads contiguous (a slice of a fused projection is
+    fine); k_cache, v_cache: [n_pages, page_size, Hkv, D] of q's type, any strides with D
+    contiguous; block_table: int32 [n_seqs, max_pages]; cu_q: int32 [n_seqs + 1], the
+    sequences' rows of q; kv_lens: int32 [n_seqs], keys in the cache, the new ones
+    included.  max_q_len: the longest sequence's rows, which chooses the kernel (None: T).
+    causal: 1 (aligned at the end) or 0.  Returns (o [T, Hq, D], lse fp32 [Hq, T] or None);
+    rows of no sequence are left as they were.  `workspace`: a CUDA byte tensor of at least
+    attn_paged_fwd_workspace_size(...) bytes; it and the outputs are allocated here if None.
+    """
+    import torch
+    device, handle = _paged_call((q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse, workspace), stream)
+    _check_cache(k_cache, v_cache)
+    n_pages, page_size, Hkv, D = k_cache.shape
+    if q.dtype not in (torch.bfloat16, torch.float16) or k_cache.dtype != q.dtype:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "q and the cache must be bf16 or float16, all one type")
+    T, Hq = q.shape[0], q.shape[1]
+    q_stride = _row_stride("q", q, Hq, D)
+    n = kv_lens.shape[0]
+    _need("kv_lens", kv_lens, torch.int32, (n,))
+    _need("cu_q", cu_q, torch.int32, (n + 1,))
+    table_stride = _check_table(block_table, n)
+    ps, ts, hs, _ = k_cache.stride()
+    with _on(device, stream):
+        if o is None:
+            o = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+        _need("o", o, q.dtype, (T, Hq, D))
+        if lse is None and want_lse:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
+        if lse is not None:
+            _need("lse", lse, torch.float32, (Hq, T))
+        if scale is None:
+            scale = 1.0 / (D ** 0.5)
+        if max_q_len is None:
+            max_q_len = T
+        if workspace is None:
+            size = attn_paged_fwd_workspace_size(T, max_q_len, Hq, Hkv, D, page_size)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        st = attn_paged_fwd_ptr(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                                0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                                kv_lens.data_ptr(), n, T, int(max_q_len), Hq, Hkv, D, n_pages, page_size,
+                                block_table.shape[1], q_stride, table_stride, ps, ts, hs, int(causal), float(scale),
+                                ATTN_DTYPE_F16 if q.dtype == torch.float16 else ATTN_DTYPE_BF16,
+                                0 if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_fwd")
+    return o, lse
 
 
 def attn_last_device_status() -> int:

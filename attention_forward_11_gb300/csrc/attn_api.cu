@@ -20,6 +20,8 @@
 #include "fmha_fwd_d256_sm103.cuh"
 #include "fmha_bwd_d256_sm103.cuh"
 #include "fmha_fwd_sm103.cuh"
+#include "paged_rows_sm103.cuh"
+#include "paged_tables_sm103.cuh"
 #include "unit_rates_sm103.cuh"
 
 namespace {
@@ -875,3 +877,5 @@ extern "C" attn_status_t attn_debug_unit_rates(double* out, int n, cudaStream_t 
     const attn_status_t now = attn_check_device_status(stream);
     return now != ATTN_OK ? now : earlier;
 }
+
+#include "paged_api.cuh"

@@ -1,0 +1,273 @@
+// paged_api.cuh -- host side of the paged key/value cache: argument checks and
+// launches of attn_paged_tables, attn_paged_append and attn_paged_fwd.  Included
+// by attn_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// Bytes from the first to one past the last element of a cache.
+size_t cache_extent(int n_pages, int page_size, int Hkv, int D, long long ps, long long ts, long long hs) {
+    return ((size_t)(n_pages - 1) * ps + (size_t)(page_size - 1) * ts + (size_t)(Hkv - 1) * hs + D) * 2;
+}
+
+// Do the three strides lay the cache's rows out without overlap?  Each axis, from the
+// one with the smallest stride up, has to step over all that lies below it.  The stride
+// of an axis of one has no meaning and becomes D.
+bool cache_layout_ok(int n_pages, int page_size, int Hkv, int D, long long& ps, long long& ts, long long& hs) {
+    if (n_pages == 1) ps = D;
+    if (page_size == 1) ts = D;
+    if (Hkv == 1) hs = D;
+    if (ps < 1 || ts < 1 || hs < 1 || ps % 8 != 0 || ts % 8 != 0 || hs % 8 != 0) return false;
+    struct Axis {
+        long long stride;
+        int n;
+    } a[3] = {{hs, Hkv}, {ts, page_size}, {ps, n_pages}};
+    std::sort(a, a + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+    long long below = D;
+    for (const Axis& x : a) {
+        if (x.n == 1) continue;
+        if (x.stride < below) return false;
+        if (x.stride > (1ll << 60) / x.n) return false;
+        below = x.stride * (x.n - 1) + below;
+    }
+    return true;
+}
+
+// Sizes of a cache and of what it is used with.
+attn_status_t check_cache(int n_pages, int page_size, int Hkv, int D, long long& ps, long long& ts, long long& hs) {
+    if (n_pages < 1 || page_size < 1 || Hkv < 1 || D < 1) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+    return cache_layout_ok(n_pages, page_size, Hkv, D, ps, ts, hs) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+bool aligned(const void* ptr, size_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; }
+
+// Shared-memory opt-in of the paged kernels, once per device.
+template <bool kF16, int kD, int kNB>
+bool opt_in_smem_rows() {
+    return cudaFuncSetAttribute(attn::paged::paged_rows_kernel<kF16, kD, kNB>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                attn::paged::RowsGeo<kD, kNB>::kSmemBytes) == cudaSuccess;
+}
+
+template <bool kF16, int kD>
+bool opt_in_smem_rows_all() {
+    return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>();
+}
+
+bool paged_device_setup(int dev, int* sm_count) {
+    static std::mutex mu;
+    static int sms[kMaxDevices] = {};
+    if (dev < 0 || dev >= kMaxDevices) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (sms[dev] == 0) {
+        int n = 0;
+        if (!opt_in_smem_rows_all<false, 64>() || !opt_in_smem_rows_all<true, 64>() ||
+            !opt_in_smem_rows_all<false, 128>() || !opt_in_smem_rows_all<true, 128>() ||
+            !opt_in_smem_rows_all<false, 256>() || !opt_in_smem_rows_all<true, 256>() ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+            return false;
+        sms[dev] = n;
+    }
+    *sm_count = sms[dev];
+    return true;
+}
+
+template <bool kF16, int kD, int kNB>
+attn_status_t launch_rows(const attn::paged::PagedParams& p, cudaStream_t stream) {
+    using G = attn::paged::RowsGeo<kD, kNB>;
+    const dim3 grid(static_cast<unsigned int>(p.Hkv), static_cast<unsigned int>(std::min(p.n_seqs, 65535)), 1);
+    attn::paged::paged_rows_kernel<kF16, kD, kNB><<<grid, G::kThreads, G::kSmemBytes, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return ATTN_OK;
+}
+
+template <bool kF16, int kD>
+attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, cudaStream_t stream) {
+    const long long rows = (long long)max_q_len * p.group;
+    return rows <= 8 ? launch_rows<kF16, kD, 1>(p, stream) : launch_rows<kF16, kD, 2>(p, stream);
+}
+
+}  // namespace
+
+extern "C" attn_status_t attn_paged_tables(const int* ctx_lens, const int* new_lens, int n_seqs, int page_size,
+                                           const int* free_pages, int n_free, const int* free_head, int* block_table,
+                                           int max_pages, long long table_stride, int* cu_new, int* kv_lens,
+                                           long long* slot_map, int max_tokens, int* counts, cudaStream_t stream) {
+    if (!ctx_lens || !new_lens || !block_table || !cu_new || !kv_lens || !slot_map || !counts) return ATTN_ERR_INVALID_ARG;
+    if (n_seqs < 1 || page_size < 1 || n_free < 0 || max_pages < 1 || max_tokens < 1) return ATTN_ERR_INVALID_ARG;
+    if (n_free > 0 && !free_pages) return ATTN_ERR_INVALID_ARG;
+    if (table_stride < max_pages || table_stride > (1ll << 60) / n_seqs) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {(const void*)ctx_lens, (const void*)new_lens, (const void*)free_pages, (const void*)free_head,
+                            (const void*)block_table, (const void*)cu_new, (const void*)kv_lens, (const void*)counts})
+        if (!aligned(ptr, 4)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(slot_map, 8)) return ATTN_ERR_INVALID_ARG;
+    const void* out_p[5] = {block_table, cu_new, kv_lens, slot_map, counts};
+    const size_t out_n[5] = {((size_t)(n_seqs - 1) * table_stride + max_pages) * 4, ((size_t)n_seqs + 1) * 4,
+                             (size_t)n_seqs * 4, (size_t)max_tokens * 8, 16};
+    const void* in_p[4] = {ctx_lens, new_lens, free_pages, free_head};
+    const size_t in_n[4] = {(size_t)n_seqs * 4, (size_t)n_seqs * 4, (size_t)n_free * 4, free_head ? 4u : 0u};
+    for (int a = 0; a < 5; ++a) {
+        for (int c = 0; c < 4; ++c)
+            if (in_n[c] > 0 && ranges_overlap(out_p[a], out_n[a], in_p[c], in_n[c])) return ATTN_ERR_INVALID_ARG;
+        for (int c = a + 1; c < 5; ++c)
+            if (ranges_overlap(out_p[a], out_n[a], out_p[c], out_n[c])) return ATTN_ERR_INVALID_ARG;
+    }
+    attn::paged::TableParams p{};
+    p.ctx_lens = ctx_lens;
+    p.new_lens = new_lens;
+    p.free_pages = free_pages;
+    p.free_head = free_head;
+    p.table = block_table;
+    p.cu_new = cu_new;
+    p.kv_lens = kv_lens;
+    p.counts = counts;
+    p.slot_map = slot_map;
+    p.table_stride = table_stride;
+    p.n_seqs = n_seqs;
+    p.n_free = n_free;
+    p.max_pages = max_pages;
+    p.max_tokens = max_tokens;
+    p.page_size = page_size;
+    p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
+    // one block per 1024 tokens, at most 128: each repeats the scan over the sequences
+    const int blocks = std::min(128, (max_tokens + attn::paged::kTableThreads - 1) / attn::paged::kTableThreads);
+    attn::paged::paged_tables_kernel<<<blocks, attn::paged::kTableThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return ATTN_OK;
+}
+
+extern "C" attn_status_t attn_paged_append(const void* k, const void* v, const long long* slot_map, void* k_cache,
+                                           void* v_cache, int n_tokens, int Hkv, int D, int n_pages, int page_size,
+                                           long long k_stride, long long v_stride, long long page_stride,
+                                           long long token_stride, long long head_stride, cudaStream_t stream) {
+    if (!k || !v || !slot_map || !k_cache || !v_cache || n_tokens < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = check_cache(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
+    if (st != ATTN_OK) return st;
+    const long long row = (long long)Hkv * D;
+    for (long long stride : {k_stride, v_stride})
+        if (stride % 8 != 0 || stride < row || stride > (1ll << 60) / n_tokens) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {k, v, (const void*)k_cache, (const void*)v_cache})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(slot_map, 8)) return ATTN_ERR_INVALID_ARG;
+    // The caches overlap no row and no slot.  K and V of one interleaved tensor share an
+    // address range without sharing an element, so the two caches are not compared.
+    const size_t cache = cache_extent(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
+    const void* in_p[3] = {k, v, slot_map};
+    const size_t in_n[3] = {((size_t)(n_tokens - 1) * k_stride + row) * 2, ((size_t)(n_tokens - 1) * v_stride + row) * 2,
+                            (size_t)n_tokens * 8};
+    for (int c = 0; c < 3; ++c)
+        if (ranges_overlap(k_cache, cache, in_p[c], in_n[c]) || ranges_overlap(v_cache, cache, in_p[c], in_n[c]))
+            return ATTN_ERR_INVALID_ARG;
+    if (k_cache == v_cache) return ATTN_ERR_INVALID_ARG;
+    if (row / 8 > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+    attn::paged::AppendParams p{};
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.k_cache = static_cast<uint16_t*>(k_cache);
+    p.v_cache = static_cast<uint16_t*>(v_cache);
+    p.slot_map = slot_map;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.page_stride = page_stride;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.n_slots = (long long)n_pages * page_size;
+    p.T = n_tokens;
+    p.row_chunks = static_cast<int>(row / 8);
+    p.head_chunks_log2 = D == 64 ? 3 : D == 128 ? 4 : 5;
+    p.per_block = std::max(1, attn::paged::kAppendThreads * 4 / p.row_chunks);
+    p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
+    p.by_row = attn::paged::make_fastdiv(static_cast<unsigned int>(p.row_chunks));
+    const unsigned int blocks = static_cast<unsigned int>(((long long)n_tokens + p.per_block - 1) / p.per_block);
+    attn::paged::paged_append_kernel<<<blocks, attn::paged::kAppendThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return ATTN_OK;
+}
+
+extern "C" attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
+                                                       size_t* bytes) {
+    if (!bytes) return ATTN_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (total_q < 1 || max_q_len < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+extern "C" attn_status_t attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                                        const int* block_table, const int* cu_q, const int* kv_lens, int n_seqs,
+                                        int total_q, int max_q_len, int Hq, int Hkv, int D, int n_pages, int page_size,
+                                        int max_pages, long long q_stride, long long table_stride,
+                                        long long page_stride, long long token_stride, long long head_stride,
+                                        int causal, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream) {
+    // ---- validation: nothing is launched on any error
+    if (!q || !k_cache || !v_cache || !o || !block_table || !cu_q || !kv_lens) return ATTN_ERR_INVALID_ARG;
+    if (n_seqs < 1 || total_q < 1 || max_q_len < 1 || Hq < 1 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = check_cache(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
+    if (st != ATTN_OK) return st;
+    if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F16) return ATTN_ERR_INVALID_ARG;
+    const long long row = (long long)Hq * D;
+    if (q_stride % 8 != 0 || q_stride < row || q_stride > (1ll << 60) / total_q) return ATTN_ERR_INVALID_ARG;
+    if (table_stride < max_pages || table_stride > (1ll << 60) / n_seqs) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k_cache, v_cache, (const void*)o})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {(const void*)lse, (const void*)block_table, (const void*)cu_q, (const void*)kv_lens})
+        if (!aligned(ptr, 4)) return ATTN_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
+    size_t need = 0;
+    const attn_status_t sw = attn_paged_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, &need);
+    if (sw == ATTN_ERR_CUDA) return sw;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+    // o, lse and the workspace overlap no input and not each other
+    const size_t cache = cache_extent(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
+    const void* out_p[3] = {o, lse, workspace};
+    const size_t out_n[3] = {(size_t)total_q * row * 2, lse ? (size_t)total_q * Hq * 4 : 0, need};
+    const void* in_p[6] = {q, k_cache, v_cache, block_table, cu_q, kv_lens};
+    const size_t in_n[6] = {((size_t)(total_q - 1) * q_stride + row) * 2, cache, cache,
+                            ((size_t)(n_seqs - 1) * table_stride + max_pages) * 4, ((size_t)n_seqs + 1) * 4, (size_t)n_seqs * 4};
+    for (int a = 0; a < 3; ++a) {
+        if (out_n[a] == 0) continue;
+        for (int c = 0; c < 6; ++c)
+            if (ranges_overlap(out_p[a], out_n[a], in_p[c], in_n[c])) return ATTN_ERR_INVALID_ARG;
+        for (int c = a + 1; c < 3; ++c)
+            if (out_n[c] > 0 && ranges_overlap(out_p[a], out_n[a], out_p[c], out_n[c])) return ATTN_ERR_INVALID_ARG;
+    }
+    attn::paged::PagedParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k_cache);
+    p.v = static_cast<const uint16_t*>(v_cache);
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.table = block_table;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
+    p.n_seqs = n_seqs;
+    p.total_q = total_q;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.group = Hq / Hkv;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.causal = causal;
+    // a length is at most what the table's columns name, and leaves room to count tiles past it
+    p.max_kv = static_cast<int>(std::min<long long>((long long)max_pages * page_size, 0x7fffffffLL - 4096));
+    p.q_stride = q_stride;
+    p.table_stride = table_stride;
+    p.page_stride = page_stride;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
+    const bool f16 = dtype == ATTN_DTYPE_F16;
+    if (D == 64) return f16 ? launch_paged<true, 64>(p, max_q_len, stream) : launch_paged<false, 64>(p, max_q_len, stream);
+    if (D == 128) return f16 ? launch_paged<true, 128>(p, max_q_len, stream) : launch_paged<false, 128>(p, max_q_len, stream);
+    return f16 ? launch_paged<true, 256>(p, max_q_len, stream) : launch_paged<false, 256>(p, max_q_len, stream);
+}

@@ -1,0 +1,64 @@
+// paged_common_sm103.cuh -- what the kernels of the paged key/value cache share:
+// the division by the page size, the launch parameters, and how a ragged batch's
+// lengths are read.
+//
+// A cache holds pages of `page_size` tokens; token t of sequence s lives at row
+// t % page_size of page table[s, t / page_size].  Lengths and tables are device
+// data that no host code sees, so every value is clamped where it is read: a
+// query range to the rows that exist, a key length to what the table's columns
+// can name, and a page that is not in [0, n_pages) holds no keys.
+#pragma once
+#include <cstdint>
+
+namespace attn {
+namespace paged {
+
+// n / d for 0 <= n < 2^64 / d as one high product: with m = floor(2^64 / d) + 1,
+// n m / 2^64 exceeds n / d by n (m d - 2^64) / (d 2^64) <= n / 2^64 < 1 / d.
+struct FastDiv {
+    unsigned long long m = 0;  // 0: the divisor is one
+    unsigned int d = 1;
+    __device__ __forceinline__ unsigned long long quot(unsigned long long n) const {
+        return m == 0 ? n : __umul64hi(n, m);
+    }
+};
+inline FastDiv make_fastdiv(unsigned int d) {
+    FastDiv f;
+    f.d = d;
+    f.m = d == 1 ? 0ull : ~0ull / d + 1;
+    return f;
+}
+
+struct PagedParams {
+    const uint16_t *q, *k, *v;  // queries [total_q, Hq, D] and the two caches
+    uint16_t* o;                // [total_q, Hq, D]
+    float* lse;                 // [Hq, total_q], or nullptr
+    const int *table, *cu_q, *kv_lens;
+    int n_seqs, total_q, Hq, Hkv, group, n_pages, page_size, max_pages, causal;
+    int max_kv;                                       // keys that a table row can name
+    long long q_stride, table_stride;                 // elements from token to token, row to row
+    long long page_stride, token_stride, head_stride;  // of both caches, in elements
+    float scale_log2;                                 // softmax scale * log2(e)
+    FastDiv by_page;
+};
+
+struct Seq {
+    int q0, q_len, kv_len;
+};
+
+__device__ __forceinline__ Seq seq_of(const PagedParams& p, int s) {
+    Seq x;
+    x.q0 = min(max(p.cu_q[s], 0), p.total_q);
+    x.q_len = max(min(p.cu_q[s + 1], p.total_q) - x.q0, 0);
+    x.kv_len = min(max(p.kv_lens[s], 0), p.max_kv);
+    return x;
+}
+
+// Keys that token t of a sequence sees: [0, visible).  Causal masks are aligned at
+// the end: the last new token sees every key.
+__device__ __forceinline__ int visible_keys(const PagedParams& p, const Seq& x, int t) {
+    return p.causal ? max(x.kv_len - x.q_len + t + 1, 0) : x.kv_len;
+}
+
+}  // namespace paged
+}  // namespace attn

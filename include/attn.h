@@ -187,6 +187,127 @@ attn_status_t attn_bwd(const void* q, const void* k, const void* v, const void* 
                        int Hkv, int D, int causal, float scale, int dtype, void* workspace,
                        size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Paged key/value cache: sequences of unlike lengths whose keys and values live in
+ * pages, for serving.  (The pages that describe this forward compute attention over
+ * dense tensors only; this is the same operation over a cache.)
+ *
+ * A cache is two tensors, K and V, of n_pages pages of page_size tokens of Hkv heads
+ * of D elements.  Element d of head h of row r of page x is at
+ *     x * page_stride + r * token_stride + h * head_stride + d   (strides in elements),
+ * so pages stored token by token ([page, token, head, D]), head by head ([page, head,
+ * token, D]) or with K and V in turn ([page, 2, token, head, D], two base pointers)
+ * are all read as they are.  K and V share the strides, which are multiples of 8 and
+ * lay no two rows over each other (of an axis of one the stride is ignored).  Base
+ * pointers are 16-byte aligned.
+ *
+ * Token t of sequence s lives in row t % page_size of page
+ * block_table[s * table_stride + t / page_size]; the table is int32 with max_pages
+ * columns.  Its slot is page * page_size + row.  An entry outside [0, n_pages) names
+ * no page: its tokens are not written and not seen.
+ *
+ * Lengths, tables and slots are device data.  No call reads them on the host, so a
+ * captured graph replays with what they hold then.  Values are clamped where they
+ * are read; no content of theirs makes a kernel leave its buffers.
+ */
+
+/*
+ * attn_paged_tables -- the tables of one step, from the lengths of its sequences.
+ *
+ * Sequence i has ctx_lens[i] tokens in the cache and gets new_lens[i] more (both
+ * device int32 [n_seqs]; a negative length counts as zero, and a sequence without new
+ * tokens takes no page).  Its row of block_table is extended by the pages that the new
+ * tokens start: columns ceil(ctx / page_size) to ceil((ctx + new) / page_size) - 1.
+ *
+ * free_pages   device int32 [n_free], pages to take in order, sequence after sequence,
+ *              from entry *free_head on (device int32; NULL: from the first).  Once
+ *              the list is used up, new columns get -1.  n_free 0 needs no list.
+ * block_table  device int32 [n_seqs, max_pages], row stride table_stride (in/out; only
+ *              the new columns are written, none past max_pages).
+ * cu_new       device int32 [n_seqs + 1] (written): sums of the new tokens before each
+ *              sequence; the batch's rows of sequence i are cu_new[i] .. cu_new[i+1]-1.
+ * kv_lens      device int32 [n_seqs] (written): ctx + new.
+ * slot_map     device int64 [max_tokens] (written): the slot of each new token, in the
+ *              batch's order; -1 for a token without a page and for every entry behind
+ *              the last token.  Tokens past max_tokens get no entry.
+ * counts       device int32 [4] (written): new tokens in all; the entry of free_pages
+ *              at which the next call starts; pages that were missing; sequences that
+ *              do not fit into max_pages columns.
+ * Sums past 2^31 - 1 are written as that.
+ *
+ * Asynchronous on `stream`, one kernel, no workspace.  int32 buffers 4-byte, slot_map
+ * 8-byte aligned; no output overlaps an input or another output; every size but
+ * n_free is at least 1.  On any error return nothing was launched.
+ */
+attn_status_t attn_paged_tables(const int* ctx_lens, const int* new_lens, int n_seqs, int page_size,
+                                const int* free_pages, int n_free, const int* free_head, int* block_table,
+                                int max_pages, long long table_stride, int* cu_new, int* kv_lens,
+                                long long* slot_map, int max_tokens, int* counts, cudaStream_t stream);
+
+/*
+ * attn_paged_append -- write the keys and values of new tokens into their pages.
+ *
+ * k, v      device pointers, 16-bit elements, [n_tokens, Hkv, D], heads contiguous, row
+ *           strides k_stride and v_stride (elements, multiples of 8, at least Hkv * D:
+ *           slices of a fused projection are read in place).
+ * slot_map  device int64 [n_tokens]: each row's slot; rows whose slot is outside
+ *           [0, n_pages * page_size) are skipped.  If two rows name one slot, the slot
+ *           holds elements of either afterwards.
+ * k_cache, v_cache, n_pages .. head_stride  the cache, as above; D 64, 128 or 256
+ *           (other head sizes: ATTN_ERR_UNSUPPORTED).  It overlaps no other argument.
+ *
+ * The rows are copied as they are (bf16 and fp16 alike).  Asynchronous on `stream`, one
+ * kernel; on any error return nothing was launched.
+ */
+attn_status_t attn_paged_append(const void* k, const void* v, const long long* slot_map, void* k_cache,
+                                void* v_cache, int n_tokens, int Hkv, int D, int n_pages, int page_size,
+                                long long k_stride, long long v_stride, long long page_stride,
+                                long long token_stride, long long head_stride, cudaStream_t stream);
+
+/*
+ * attn_paged_fwd -- attn_fwd for the new tokens of a ragged batch over their cache:
+ * whole prompts, chunks of prompts, drafted tokens and single tokens, in one call.
+ *
+ * q            device pointer, [total_q, Hq, D], heads contiguous, row stride q_stride
+ *              (elements, a multiple of 8, at least Hq * D), 16-byte aligned.
+ * o            device pointer, [total_q, Hq, D] contiguous, 16-byte aligned (written).
+ * lse          device pointer, fp32 [Hq, total_q], or NULL to skip it (written).
+ * cu_q         device int32 [n_seqs + 1]: sequence i's rows of q and o are cu_q[i] ..
+ *              cu_q[i+1] - 1, cut to [0, total_q); a sequence may have none.  Rows of no
+ *              sequence (behind the last one, in a padded batch) are left as they were.
+ * kv_lens      device int32 [n_seqs]: keys of sequence i in the cache, its new tokens
+ *              among them (append before this call); values below zero count as zero,
+ *              values past max_pages * page_size as that.
+ * block_table, k_cache, v_cache, n_pages .. head_stride  the cache, as above.
+ * max_q_len    the longest sequence's rows, >= 1, as far as the host knows.  It chooses
+ *              the kernel (few rows against many); results are right for any value.
+ * causal       0: every key of the sequence is visible.  1: row t of a sequence with n
+ *              rows and m keys sees keys j <= t + (m - n).  A row that sees no key gets
+ *              O = 0 and LSE = -inf.  What unseen rows of the cache hold (stale rows
+ *              behind the last key, NaN or infinities among them) has no influence; a
+ *              key that some rows of a sequence see and others do not is expected to be
+ *              finite.
+ * Hq, Hkv, D, scale, dtype  as attn_fwd_ex.
+ * workspace    device pointer, 256-byte aligned, of at least
+ *              attn_paged_fwd_workspace_size bytes for the current device, or NULL when
+ *              that is 0.  Scratch: its contents are undefined before and after the
+ *              call, and calls that overlap in time on the GPU must not share one.
+ *
+ * Arithmetic as attn_fwd: operands and P in the element type, products and softmax
+ * statistics in fp32, O rounded to nearest even once.  Results do not depend on timing:
+ * two calls with equal arguments give equal bits.  Asynchronous on `stream`; o, lse and
+ * the workspace overlap no input and not each other.  On any error return nothing was
+ * launched; a device-side timeout shows in attn_last_device_status.
+ */
+attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
+                                            size_t* bytes);
+attn_status_t attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                             const int* block_table, const int* cu_q, const int* kv_lens, int n_seqs,
+                             int total_q, int max_q_len, int Hq, int Hkv, int D, int n_pages, int page_size,
+                             int max_pages, long long q_stride, long long table_stride, long long page_stride,
+                             long long token_stride, long long head_stride, int causal, float scale, int dtype,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* attn_status_str(attn_status_t status);
 

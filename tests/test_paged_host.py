@@ -1,0 +1,127 @@
+"""CPU-only checks of the paged cache's entry points: host-side validation rejects
+bad requests before any CUDA call, and the plain implementation that the GPU tests
+compare with agrees with attention over dense tensors."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_forward_11_gb300 as fa
+import oracle
+from attention_forward_11_gb300 import build as fa_build
+from paged_ref import Batch, plain_tables
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    fa_build.build()
+    oracle.build()
+    return fa.load_library()
+
+
+A = [0x10000000 * (i + 1) for i in range(16)]  # fake, aligned, far apart; never dereferenced
+BIG = 1 << 40
+
+TABLES = dict(ctx=A[0], new=A[1], n_seqs=4, page=16, free=A[2], n_free=100, head=A[3], table=A[4], max_pages=50,
+              table_stride=50, cu=A[5], kv=A[6], slots=A[7], max_tokens=300, counts=A[8], stream=0)
+APPEND = dict(k=A[0], v=A[1], slots=A[2], kc=A[3], vc=A[4], T=7, Hkv=2, D=128, n_pages=9, page=16, ks=256, vs=256,
+              ps=16 * 256, ts=256, hs=128, stream=0)
+FWD = dict(q=A[0], kc=A[1], vc=A[2], o=A[3], lse=A[4], table=A[5], cu=A[6], kv=A[7], n_seqs=4, T=40, max_q=10, Hq=4,
+           Hkv=2, D=128, n_pages=9, page=16, max_pages=5, qs=512, table_stride=5, ps=16 * 256, ts=256, hs=128, causal=1,
+           scale=0.088, dtype=0, ws=A[8], ws_bytes=BIG, stream=0)
+
+
+def ids(d):
+    return ",".join(f"{k}={v}" for k, v in d.items())
+
+
+@pytest.mark.parametrize("over", [
+    dict(ctx=0), dict(new=0), dict(table=0), dict(cu=0), dict(kv=0), dict(slots=0), dict(counts=0), dict(free=0),
+    dict(n_seqs=0), dict(page=0), dict(n_free=-1), dict(max_pages=0), dict(max_tokens=0), dict(max_tokens=-5),
+    dict(table_stride=49), dict(table_stride=1 << 62), dict(ctx=A[0] + 2), dict(slots=A[7] + 4), dict(head=A[3] + 1),
+    dict(table=A[0]), dict(cu=A[1] + 4), dict(kv=A[4] + 8), dict(slots=A[2] + 8), dict(counts=A[3]),
+    dict(counts=A[7] + 8 * 299), dict(free=A[4] + 4 * 199),
+], ids=ids)
+def test_tables_refusals(over):
+    assert fa.attn_paged_tables_ptr(*{**TABLES, **over}.values()) == fa.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    dict(k=0), dict(v=0), dict(slots=0), dict(kc=0), dict(vc=0), dict(T=0), dict(Hkv=0), dict(D=0), dict(n_pages=0),
+    dict(page=0), dict(ks=248), dict(vs=260), dict(ks=-256), dict(ps=0), dict(ts=128), dict(hs=64), dict(hs=132),
+    dict(ps=16 * 256 - 8), dict(k=A[0] + 8), dict(kc=A[3] + 2), dict(slots=A[2] + 4), dict(vc=A[3]),
+    dict(k=A[3] + 16 * 256), dict(slots=A[4] + 8), dict(ps=1 << 61),
+], ids=ids)
+def test_append_refusals(over):
+    assert fa.attn_paged_append_ptr(*{**APPEND, **over}.values()) == fa.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=0), dict(kc=0), dict(vc=0), dict(o=0), dict(table=0), dict(cu=0), dict(kv=0), dict(n_seqs=0), dict(T=0),
+    dict(max_q=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(D=0), dict(n_pages=0), dict(page=0), dict(max_pages=0),
+    dict(qs=504), dict(qs=516), dict(table_stride=4), dict(ps=8), dict(ts=8), dict(hs=0), dict(causal=2),
+    dict(causal=-1), dict(scale=0.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=-1.0), dict(dtype=2),
+    dict(q=A[0] + 8), dict(kc=A[1] + 4), dict(o=A[3] + 2), dict(lse=A[4] + 2), dict(table=A[5] + 2), dict(cu=A[6] + 1),
+    dict(o=A[0]), dict(o=A[1] + 64), dict(o=A[2]), dict(lse=A[3] + 16), dict(lse=A[5]), dict(o=A[6] - 4096),
+    dict(ws=A[8] + 16),
+], ids=ids)
+def test_fwd_refusals(over):
+    assert fa.attn_paged_fwd_ptr(*{**FWD, **over}.values()) == fa.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("D", [32, 96, 192, 320])
+def test_other_head_sizes_unsupported(D):
+    assert fa.attn_paged_append_ptr(*{**APPEND, "D": D}.values()) == fa.ATTN_ERR_UNSUPPORTED
+    assert fa.attn_paged_fwd_ptr(*{**FWD, "D": D}.values()) == fa.ATTN_ERR_UNSUPPORTED
+    with pytest.raises(fa.AttnError) as e:
+        fa.attn_paged_fwd_workspace_size(40, 10, 4, 2, D, 16)
+    assert e.value.status == fa.ATTN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("args", [(0, 1, 4, 2, 128, 16), (4, 0, 4, 2, 128, 16), (4, 1, 3, 2, 128, 16),
+                                  (4, 1, 4, 0, 128, 16), (4, 1, 4, 2, 128, 0), (4, 1, 4, 2, 0, 16)])
+def test_workspace_size_refusals(args):
+    with pytest.raises(fa.AttnError) as e:
+        fa.attn_paged_fwd_workspace_size(*args)
+    assert e.value.status == fa.ATTN_ERR_INVALID_ARG
+
+
+def test_binding_refuses_host_tensors():
+    b = Batch([(20, 3)], 4, 2, 64, 16, device="cpu")
+    with pytest.raises(fa.AttnError) as e:
+        fa.attn_paged_fwd(**b.on_gpu())
+    assert e.value.status == fa.ATTN_ERR_INVALID_ARG
+    with pytest.raises(fa.AttnError):
+        fa.attn_paged_append(b.q[:, :2], b.q[:, :2], torch.zeros(3, dtype=torch.int64), b.k_cache, b.v_cache)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(fa.AttnError):
+        fa.attn_paged_tables(i, i, i, b.table, 16, 4)
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("layout", ["tokens", "heads", "turns"])
+def test_plain_attention_is_the_dense_one(causal, layout):
+    """The paged reference against the framework's 64-bit oracle, sequence by sequence."""
+    lens = [(70, 5), (16, 16), (33, 1), (4, 9)]
+    b = Batch(lens, 4, 2, 64, 16, causal=causal, layout=layout, device="cpu", seed=3)
+    o, lse, _, _ = b.reference()
+    for s, (kv, n) in enumerate(lens):
+        pages = b.table[s, :-(-kv // 16)].long()
+        k, v = (c[pages].reshape(-1, 2, 64)[:kv] for c in (b.k_cache, b.v_cache))
+        assert torch.equal(k, b.dense[s][0]) and torch.equal(v, b.dense[s][1])
+        a = b.cu[s]
+        bits = [np.ascontiguousarray(x[None].contiguous().view(torch.int16).numpy()).view(np.uint16)
+                for x in (b.q[a:a + n], k, v)]
+        ro, rl = oracle.attn_full(*bits, causal, b.scale)
+        assert np.abs(o[a:a + n] - ro[0]).max() < 1e-6
+        assert np.array_equal(np.isneginf(lse[:, a:a + n]), np.isneginf(rl[0]))
+        fin = ~np.isneginf(rl[0])
+        assert np.abs(lse[:, a:a + n][fin] - rl[0][fin]).max() < 1e-6
+
+
+def test_plain_tables_by_hand():
+    table, cu, kv, slots, counts = plain_tables([3, 0, 4], [3, 0, 1], [7, 8, 9], 1, [[5, -1], [-1, -1], [6, -1]], 4, 6)
+    assert table == [[5, 8], [-1, -1], [6, 9]]
+    assert cu == [0, 3, 3, 4] and kv == [6, 0, 5] and counts == [4, 3, 0, 0]
+    assert slots == [5 * 4 + 3, 8 * 4, 8 * 4 + 1, 9 * 4, -1, -1]
