@@ -21,6 +21,7 @@
 #include "fmha_bwd_d256_sm103.cuh"
 #include "fmha_fwd_sm103.cuh"
 #include "paged_rows_sm103.cuh"
+#include "paged_sched_sm103.cuh"
 #include "paged_tables_sm103.cuh"
 #include "unit_rates_sm103.cuh"
 

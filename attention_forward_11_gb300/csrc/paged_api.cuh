@@ -52,7 +52,8 @@ bool opt_in_smem_rows() {
 
 template <bool kF16, int kD>
 bool opt_in_smem_rows_all() {
-    return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>();
+    if constexpr (kD == 256) return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>();
+    else return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() && opt_in_smem_rows<kF16, kD, 4>();
 }
 
 bool paged_device_setup(int dev, int* sm_count) {
@@ -73,20 +74,64 @@ bool paged_device_setup(int dev, int* sm_count) {
     return true;
 }
 
-template <bool kF16, int kD, int kNB>
-attn_status_t launch_rows(const attn::paged::PagedParams& p, cudaStream_t stream) {
-    using G = attn::paged::RowsGeo<kD, kNB>;
-    const dim3 grid(static_cast<unsigned int>(p.Hkv), static_cast<unsigned int>(std::min(p.n_seqs, 65535)), 1);
-    attn::paged::paged_rows_kernel<kF16, kD, kNB><<<grid, G::kThreads, G::kSmemBytes, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+// The workspace's parts, for blocks of `rows` rows.
+attn::paged::Workspace split_workspace(void* workspace, int sms, int rows) {
+    using namespace attn::paged;
+    char* at = static_cast<char*>(workspace);
+    Workspace w;
+    w.header = reinterpret_cast<PieceHeader*>(at);
+    w.ml = reinterpret_cast<float2*>(at + ws_header_bytes(sms));
+    w.o = reinterpret_cast<float*>(at + ws_header_bytes(sms) + ws_ml_bytes(sms, rows));
+    return w;
+}
+
+// 8-row blocks of the rows kernel for sequences of at most `rows` (token, head) rows a
+// key/value head.  At head size 256 four blocks' sums do not fit the registers.
+int row_blocks_for(long long rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
+
+// Launched so that its blocks are in place while the first kernel's still run; they wait
+// for its end before they read.
+template <class Kernel>
+attn_status_t launch_behind(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, const attn::paged::PagedParams& p,
+                            const attn::paged::SchedParams& sp) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, p, sp) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return ATTN_OK;
 }
 
+template <bool kF16, int kD, int kNB>
+attn_status_t launch_rows(const attn::paged::PagedParams& p, void* workspace, int sms, cudaStream_t stream) {
+    using namespace attn::paged;
+    using G = RowsGeo<kD, kNB>;
+    SchedParams sp{};
+    sp.map = make_row_map(p.Hkv, p.group, G::kRows, 1);
+    sp.ws = split_workspace(workspace, sms, G::kRows);
+    paged_rows_kernel<kF16, kD, kNB><<<sms, G::kThreads, G::kSmemBytes, stream>>>(p, sp);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    // one row a block: a long sequence alone has as many pieces as there are SMs
+    return launch_behind(paged_combine_kernel<kF16, kD, G::kRows, 1, 1>, dim3(sms, G::kRows), kCombineThreads, stream, p, sp);
+}
+
 template <bool kF16, int kD>
-attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, cudaStream_t stream) {
-    const long long rows = (long long)max_q_len * p.group;
-    return rows <= 8 ? launch_rows<kF16, kD, 1>(p, stream) : launch_rows<kF16, kD, 2>(p, stream);
+attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
+    const int nb = row_blocks_for((long long)max_q_len * p.group, kD);
+    if (nb == 1) return launch_rows<kF16, kD, 1>(p, workspace, sms, stream);
+    if constexpr (kD != 256)
+        if (nb == 4) return launch_rows<kF16, kD, 4>(p, workspace, sms, stream);
+    return launch_rows<kF16, kD, 2>(p, workspace, sms, stream);
 }
 
 }  // namespace
@@ -194,6 +239,10 @@ extern "C" attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_le
     *bytes = 0;
     if (total_q < 1 || max_q_len < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
     if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)total_q * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
+    *bytes = attn::paged::ws_bytes(sms, 8 * row_blocks_for((long long)max_q_len * (Hq / Hkv), D), D);
     return ATTN_OK;
 }
 
@@ -221,7 +270,7 @@ extern "C" attn_status_t attn_paged_fwd(const void* q, const void* k_cache, cons
     if (workspace && !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
     size_t need = 0;
     const attn_status_t sw = attn_paged_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, &need);
-    if (sw == ATTN_ERR_CUDA) return sw;
+    if (sw != ATTN_OK) return sw;
     if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
     // o, lse and the workspace overlap no input and not each other
     const size_t cache = cache_extent(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
@@ -267,7 +316,7 @@ extern "C" attn_status_t attn_paged_fwd(const void* q, const void* k_cache, cons
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
     const bool f16 = dtype == ATTN_DTYPE_F16;
-    if (D == 64) return f16 ? launch_paged<true, 64>(p, max_q_len, stream) : launch_paged<false, 64>(p, max_q_len, stream);
-    if (D == 128) return f16 ? launch_paged<true, 128>(p, max_q_len, stream) : launch_paged<false, 128>(p, max_q_len, stream);
-    return f16 ? launch_paged<true, 256>(p, max_q_len, stream) : launch_paged<false, 256>(p, max_q_len, stream);
+    if (D == 64) return f16 ? launch_paged<true, 64>(p, max_q_len, workspace, sms, stream) : launch_paged<false, 64>(p, max_q_len, workspace, sms, stream);
+    if (D == 128) return f16 ? launch_paged<true, 128>(p, max_q_len, workspace, sms, stream) : launch_paged<false, 128>(p, max_q_len, workspace, sms, stream);
+    return f16 ? launch_paged<true, 256>(p, max_q_len, workspace, sms, stream) : launch_paged<false, 256>(p, max_q_len, workspace, sms, stream);
 }

@@ -13,11 +13,17 @@
 // (online softmax in log2 units, fp32), so warps meet only at the end of a unit, where
 // their (m, l, O) are merged in a fixed order.  P is rounded to the operands' type for
 // its product, as in the dense forward.
+//
+// One block a SM takes an equal share of the batch (paged_sched_sm103.cuh).  Each warp
+// fills a ring of its own with cp.async, kStages - 1 slices ahead of the one it computes
+// and across the ends of units, with no barrier between warps: 16-byte copies follow any
+// page size and any strides, and a slice's page numbers are read one slice earlier still.
 #pragma once
 #include <cmath>
 #include <cstdint>
 
 #include "paged_common_sm103.cuh"
+#include "paged_sched_sm103.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -78,49 +84,114 @@ struct RowsGeo {
     static constexpr int kTileKeys = 16 * kWarps;       // keys of all warps in one step
     static constexpr int kSliceBytes = 16 * kD * 2;     // K or V rows of one warp's step
     static constexpr int kChunks = kD / 8;              // 16-byte pieces of a row
-    static constexpr int kMergeStride = kD + 4;         // floats; rows 2t of a warp fall into different banks
-    static constexpr int kRing = kWarps * 2 * kSliceBytes;
+    static constexpr int kStages = kD == 64 ? 6 : 3;    // 192 KB of slices
+    static constexpr int kMergeCols = 64;               // columns of O merged at a time
+    static constexpr int kMergeStride = kMergeCols + 4; // floats; rows 2 t of a warp fall into different banks
+    static constexpr int kRing = kWarps * kStages * 2 * kSliceBytes;
     static constexpr int kMerge = kWarps * 8 * kMergeStride * 4;
     static constexpr int kStats = kWarps * kRows * 8;
     static constexpr int kSmemBytes = kRing + kMerge + kStats;
+    static_assert(kSmemBytes <= 231000, "ring, merge buffer and static shared memory exceed 227 KB");
+    // a piece is worth its merge from two tiles on, a share from four
+    static constexpr int kMinPiece = 2, kMinShare = 4;
+    using ShareT = Share<kTileKeys, kMinPiece, kMinShare>;
+    using CursorT = Cursor<ShareT, kTileKeys>;
 };
 
 template <bool kF16, int kD, int kNB>
-__global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1) paged_rows_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
+    paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ SchedParams sp) {
     using G = RowsGeo<kD, kNB>;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_part[G::kWarps];
+    __shared__ StartPos s_start;
+    __shared__ uint32_t s_valid[G::kWarps][G::kStages];  // keys of a slice that have a page
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * 2 * G::kSliceBytes;
+    const uint32_t ring = smem_u32(smem) + warp * (G::kStages * 2 * G::kSliceBytes);
     float* merge = reinterpret_cast<float*>(smem + G::kRing);
     float2* stats = reinterpret_cast<float2*>(smem + G::kRing + G::kMerge);
-    const int hkv = blockIdx.x;
-    for (int s = blockIdx.y; s < p.n_seqs; s += gridDim.y) {
-    const Seq x = seq_of(p, s);
-    const long long n_rows = (long long)x.q_len * p.group;
-    for (long long row0 = (long long)blockIdx.z * G::kRows; row0 < n_rows; row0 += (long long)gridDim.z * G::kRows) {
+    launch_dependents();
+
+    typename G::ShareT sh;
+    if (tid == 0) sp.ws.header[blockIdx.x].n = 0;
+    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare>(p, sp, s_part, &s_start, sh);
+    if (!some) return;
+    typename G::CursorT cur;
+    cur.first(p, sp, sh, s_start);
+    typename G::CursorT ld = cur;  // the copies' position, ahead of the products'
+    int ld_tile = ld.tile;
+
+    // The page numbers of the next slice to copy: lane i has that of key i % 16.
+    int page = -1, page_row = 0;
+    auto look_up = [&]() {
+        page = -1;
+        if (!ld.ok) return;
+        const int key = ld_tile * G::kTileKeys + 16 * warp + (lane & 15);
+        if (key >= ld.keys) return;
+        const int col = static_cast<int>(p.by_page.quot(key));
+        page = p.table[ld.s * p.table_stride + col];
+        page_row = key - col * p.page_size;
+    };
+    // Copies that slice into a stage, then moves on.
+    auto issue = [&](int st) {
+        if (ld.ok) {
+            const bool there = page >= 0 && page < p.n_pages;
+            const long long base = there ? page * p.page_stride + page_row * p.token_stride +
+                                               ld.head_unit / sp.map.splits * p.head_stride
+                                         : 0;
+            const uint32_t valid = __ballot_sync(0xffffffffu, there) & 0xffffu;
+            if (lane == 0) s_valid[warp][st] = valid;
+            const uint32_t to = ring + st * (2 * G::kSliceBytes);
+            if (ld_tile * G::kTileKeys + 16 * warp < ld.keys) {
+#pragma unroll
+                for (int i = 0; i < G::kChunks / 2; ++i) {
+                    const int idx = lane + 32 * i, kk = idx / G::kChunks, ch = idx % G::kChunks;
+                    const long long at = __shfl_sync(0xffffffffu, base, kk) + ch * 8;
+                    const bool ok = (valid >> kk) & 1;
+                    const uint32_t dst = to + kk * (kD * 2) + ((ch ^ (kk & 7)) << 4);
+                    cp_async16(dst, p.k + at, ok);
+                    cp_async16(dst + G::kSliceBytes, p.v + at, ok);
+                }
+            }
+            if (++ld_tile == ld.tile_end) {
+                ld.next(p, sp, sh);
+                ld_tile = ld.tile;
+            }
+            look_up();
+        }
+        cp_async_commit();
+    };
+    look_up();
+#pragma unroll 1
+    for (int st = 0; st < G::kStages; ++st) issue(st);
+    int st = 0;
+
+#pragma unroll 1
+    for (; cur.ok; cur.next(p, sp, sh)) {
+        const Seq x = cur.x;
+        const int t0 = cur.row_unit * sp.map.tokens;
         // Q^T as the products' B operand: row n0 + g, elements 16 ks + 2 t4 (+ 8)
         uint32_t qf[kNB][kD / 16][2];
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
-            const long long r = row0 + 8 * nb + g;
-            const bool there = r < n_rows;
-            const uint16_t* src = p.q + (there ? (x.q0 + r / p.group) * p.q_stride + (hkv * p.group + r % p.group) * kD : 0);
+            const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + g);
+            const uint16_t* src = p.q + (w.there ? (x.q0 + w.token) * p.q_stride + w.head * kD : 0);
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
-                qf[nb][ks][0] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * t4) : 0u;
-                qf[nb][ks][1] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 + 2 * t4) : 0u;
+                qf[nb][ks][0] = w.there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * t4) : 0u;
+                qf[nb][ks][1] = w.there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 + 2 * t4) : 0u;
             }
         }
         // this thread's two rows of every row block: 2 t4 and 2 t4 + 1
-        int lim[kNB][2], last = 0;
+        int lim[kNB][2];
         float m[kNB][2], l[kNB][2], o[kNB][kD / 16][4];
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const long long r = row0 + 8 * nb + 2 * t4 + e;
-                lim[nb][e] = r < n_rows ? visible_keys(p, x, static_cast<int>(r / p.group)) : 0;
+                const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + 2 * t4 + e);
+                lim[nb][e] = w.there ? visible_keys(p, x, w.token) : 0;
                 m[nb][e] = -INFINITY;
                 l[nb][e] = 0.f;
             }
@@ -130,95 +201,80 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1) paged_rows_kern
             for (int mt = 0; mt < kD / 16; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nb][mt][e] = 0.f;
-        last = visible_keys(p, x, static_cast<int>(min(row0 + G::kRows, n_rows) - 1) / p.group);  // of the last row
 
-        for (int k0 = 16 * warp; k0 < last; k0 += G::kTileKeys) {
-            // lane i < 16 looks up key k0 + i; a key without a page is zero and masked
-            long long base = 0;
-            bool there = false;
-            const int key = k0 + (lane & 15);
-            if (key < last) {
-                const int col = static_cast<int>(p.by_page.quot(key));
-                const int page = p.table[s * p.table_stride + col];
-                there = page >= 0 && page < p.n_pages;
-                if (there) base = page * p.page_stride + (key - col * p.page_size) * p.token_stride + hkv * p.head_stride;
-            }
-            const uint32_t valid = __ballot_sync(0xffffffffu, there);
-#pragma unroll
-            for (int i = 0; i < G::kChunks / 2; ++i) {
-                const int idx = lane + 32 * i, kk = idx / G::kChunks, ch = idx % G::kChunks;
-                const long long at = __shfl_sync(0xffffffffu, base, kk) + ch * 8;
-                const bool ok = (valid >> kk) & 1;
-                const uint32_t dst = ring + kk * (kD * 2) + ((ch ^ (kk & 7)) << 4);
-                cp_async16(dst, p.k + at, ok);
-                cp_async16(dst + G::kSliceBytes, p.v + at, ok);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
+#pragma unroll 1
+        for (int tile = cur.tile; tile < cur.tile_end; ++tile) {
+            cp_async_wait<G::kStages - 1>();
             __syncwarp();
-
-            float sc[kNB][4];
+            const int k0 = tile * G::kTileKeys + 16 * warp;
+            const uint32_t from = ring + st * (2 * G::kSliceBytes);
+            const uint32_t valid = s_valid[warp][st];
+            if (k0 < cur.keys) {
+                float sc[kNB][4];
 #pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
-            {
-                const int kk = (lane & 7) + ((lane >> 3) & 1) * 8;
-                const uint32_t a0 = ring + kk * (kD * 2);
+                for (int nb = 0; nb < kNB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+                {
+                    const int kk = (lane & 7) + ((lane >> 3) & 1) * 8;
+                    const uint32_t a0 = from + kk * (kD * 2);
 #pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    uint32_t a[4];
-                    ldsm_x4(a, a0 + (((2 * ks + (lane >> 4)) ^ (kk & 7)) << 4));
+                    for (int ks = 0; ks < kD / 16; ++ks) {
+                        uint32_t a[4];
+                        ldsm_x4(a, a0 + (((2 * ks + (lane >> 4)) ^ (kk & 7)) << 4));
 #pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(sc[nb], a, qf[nb][ks][0], qf[nb][ks][1]);
+                        for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(sc[nb], a, qf[nb][ks][0], qf[nb][ks][1]);
+                    }
+                }
+                uint32_t pf[kNB][2];
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb) {
+                    // element e of sc: key k0 + g + 8 (e / 2), row 2 t4 + e % 2
+                    float al[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool v0 = ((valid >> g) & 1) && k0 + g < lim[nb][e];
+                        const bool v1 = ((valid >> (g + 8)) & 1) && k0 + g + 8 < lim[nb][e];
+                        float a = v0 ? sc[nb][e] * p.scale_log2 : -INFINITY;
+                        float b = v1 ? sc[nb][e + 2] * p.scale_log2 : -INFINITY;
+                        float mx = fmaxf(a, b);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float mn = fmaxf(m[nb][e], mx), use = mn == -INFINITY ? 0.f : mn;
+                        al[e] = ex2_approx(m[nb][e] - use);
+                        m[nb][e] = mn;
+                        a = ex2_approx(a - use);
+                        b = ex2_approx(b - use);
+                        l[nb][e] = l[nb][e] * al[e] + (a + b);
+                        sc[nb][e] = a;
+                        sc[nb][e + 2] = b;
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < kD / 16; ++mt) {
+                        o[nb][mt][0] *= al[0];
+                        o[nb][mt][1] *= al[1];
+                        o[nb][mt][2] *= al[0];
+                        o[nb][mt][3] *= al[1];
+                    }
+                    pf[nb][0] = movmatrix(pack_x2<kF16>(sc[nb][0], sc[nb][1]));
+                    pf[nb][1] = movmatrix(pack_x2<kF16>(sc[nb][2], sc[nb][3]));
+                }
+                {
+                    const int kk = (lane & 7) + (lane >> 4) * 8;
+                    const uint32_t a0 = from + G::kSliceBytes + kk * (kD * 2);
+#pragma unroll
+                    for (int mt = 0; mt < kD / 16; ++mt) {
+                        uint32_t a[4];
+                        ldsm_x4_trans(a, a0 + (((2 * mt + ((lane >> 3) & 1)) ^ (kk & 7)) << 4));
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(o[nb][mt], a, pf[nb][0], pf[nb][1]);
+                    }
                 }
             }
-            uint32_t pf[kNB][2];
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) {
-                // element e of sc: key k0 + g + 8 (e / 2), row 2 t4 + e % 2
-                float al[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool v0 = ((valid >> g) & 1) && k0 + g < lim[nb][e];
-                    const bool v1 = ((valid >> (g + 8)) & 1) && k0 + g + 8 < lim[nb][e];
-                    float a = v0 ? sc[nb][e] * p.scale_log2 : -INFINITY;
-                    float b = v1 ? sc[nb][e + 2] * p.scale_log2 : -INFINITY;
-                    float mx = fmaxf(a, b);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[nb][e], mx), use = mn == -INFINITY ? 0.f : mn;
-                    al[e] = exp2f(m[nb][e] - use);
-                    m[nb][e] = mn;
-                    a = exp2f(a - use);
-                    b = exp2f(b - use);
-                    l[nb][e] = l[nb][e] * al[e] + (a + b);
-                    sc[nb][e] = a;
-                    sc[nb][e + 2] = b;
-                }
-#pragma unroll
-                for (int mt = 0; mt < kD / 16; ++mt) {
-                    o[nb][mt][0] *= al[0];
-                    o[nb][mt][1] *= al[1];
-                    o[nb][mt][2] *= al[0];
-                    o[nb][mt][3] *= al[1];
-                }
-                pf[nb][0] = movmatrix(pack_x2<kF16>(sc[nb][0], sc[nb][1]));
-                pf[nb][1] = movmatrix(pack_x2<kF16>(sc[nb][2], sc[nb][3]));
-            }
-            {
-                const int kk = (lane & 7) + (lane >> 4) * 8;
-                const uint32_t a0 = ring + G::kSliceBytes + kk * (kD * 2);
-#pragma unroll
-                for (int mt = 0; mt < kD / 16; ++mt) {
-                    uint32_t a[4];
-                    ldsm_x4_trans(a, a0 + (((2 * mt + ((lane >> 3) & 1)) ^ (kk & 7)) << 4));
-#pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(o[nb][mt], a, pf[nb][0], pf[nb][1]);
-                }
-            }
-            __syncwarp();
+            __syncwarp();  // every lane has read the stage and its mask
+            issue(st);
+            st = st + 1 == G::kStages ? 0 : st + 1;
         }
 
-        // merge the warps: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L
+        // merge the warps: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) (/ L when the unit is whole)
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
@@ -227,49 +283,64 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1) paged_rows_kern
                 for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
                 if (g == 0) stats[warp * G::kRows + 8 * nb + 2 * t4 + e] = make_float2(m[nb][e], l[nb][e]);
             }
+        const bool whole = cur.whole();
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (cur.tile == 0 ? 1 : 0);
+        if (!whole && cur.tile == 0 && tid == 0)
+            sp.ws.header[blockIdx.x] = PieceHeader{sh.pieces(cur.at, cur.tiles, static_cast<int>(blockIdx.x)), cur.s,
+                                                   cur.head_unit, cur.row_unit};
+        constexpr int kParts = kD / G::kMergeCols;
 #pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) {
-            __syncthreads();  // the stats are there; the rows before have been read
+        for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-            for (int mt = 0; mt < kD / 16; ++mt)
+            for (int part = 0; part < kParts; ++part) {
+                __syncthreads();  // the stats are there; what was merged before has been read
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    merge[(warp * 8 + 2 * t4 + (e & 1)) * G::kMergeStride + 16 * mt + g + 8 * (e >> 1)] = o[nb][mt][e];
-            __syncthreads();
-            for (int i = tid; i < 8 * (kD / 4); i += G::kThreads) {
-                const int r = i / (kD / 4), d = (i % (kD / 4)) * 4;
-                const long long row = row0 + 8 * nb + r;
-                if (row >= n_rows) continue;
-                float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+                for (int mt = 0; mt < G::kMergeCols / 16; ++mt)
 #pragma unroll
-                for (int w = 0; w < G::kWarps; ++w) M = fmaxf(M, stats[w * G::kRows + 8 * nb + r].x);
-                const float use = M == -INFINITY ? 0.f : M;
+                    for (int e = 0; e < 4; ++e)
+                        merge[(warp * 8 + 2 * t4 + (e & 1)) * G::kMergeStride + 16 * mt + g + 8 * (e >> 1)] =
+                            o[nb][part * (G::kMergeCols / 16) + mt][e];
+                __syncthreads();
 #pragma unroll
-                for (int w = 0; w < G::kWarps; ++w) {
-                    const float2 ml = stats[w * G::kRows + 8 * nb + r];
-                    const float f = exp2f(ml.x - use);
-                    const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + r) * G::kMergeStride + d);
-                    L += ml.y * f;
-                    a0 += v.x * f;
-                    a1 += v.y * f;
-                    a2 += v.z * f;
-                    a3 += v.w * f;
+                for (int i = tid; i < 8 * (G::kMergeCols / 4); i += G::kThreads) {
+                    const int r = i / (G::kMergeCols / 4), dc = (i % (G::kMergeCols / 4)) * 4, d = part * G::kMergeCols + dc;
+                    const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + r);
+                    if (!w.there) continue;
+                    float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+                    for (int k = 0; k < G::kWarps; ++k) M = fmaxf(M, stats[k * G::kRows + 8 * nb + r].x);
+                    const float use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                    for (int k = 0; k < G::kWarps; ++k) {
+                        const float2 ml = stats[k * G::kRows + 8 * nb + r];
+                        const float f = ex2_approx(ml.x - use);
+                        const float4 v = *reinterpret_cast<const float4*>(merge + (k * 8 + r) * G::kMergeStride + dc);
+                        L += ml.y * f;
+                        a0 += v.x * f;
+                        a1 += v.y * f;
+                        a2 += v.z * f;
+                        a3 += v.w * f;
+                    }
+                    if (whole) {
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        const long long tok = x.q0 + w.token;
+                        uint2 out;
+                        out.x = pack_x2<kF16>(a0 * inv, a1 * inv);
+                        out.y = pack_x2<kF16>(a2 * inv, a3 * inv);
+                        *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + d) = out;
+                        if (d == 0 && p.lse != nullptr)
+                            p.lse[(long long)w.head * p.total_q + tok] =
+                                L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                    } else {
+                        const size_t row = (size_t)slot * G::kRows + 8 * nb + r;
+                        *reinterpret_cast<float4*>(sp.ws.o + row * kD + d) = make_float4(a0, a1, a2, a3);
+                        if (d == 0) sp.ws.ml[row] = make_float2(M, L);
+                    }
                 }
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                const long long tok = x.q0 + row / p.group;
-                const int hq = hkv * p.group + static_cast<int>(row % p.group);
-                uint2 out;
-                out.x = pack_x2<kF16>(a0 * inv, a1 * inv);
-                out.y = pack_x2<kF16>(a2 * inv, a3 * inv);
-                *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + hq) * kD + d) = out;
-                if (d == 0 && p.lse != nullptr)
-                    p.lse[(long long)hq * p.total_q + tok] =
-                        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
             }
-        }
-        __syncthreads();
+        __syncthreads();  // the stats may be overwritten
     }
-    }
+    cp_async_wait<0>();
 }
 
 }  // namespace paged
