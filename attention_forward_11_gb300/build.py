@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "attn_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("fmha_fwd_sm103.cuh", "fmha_fwd_d256_sm103.cuh", "fmha_bwd_sm103.cuh",
                                           "fmha_bwd_d256_sm103.cuh", "paged_common_sm103.cuh", "paged_tables_sm103.cuh",
-                                          "paged_sched_sm103.cuh", "paged_rows_sm103.cuh", "paged_api.cuh", "unit_rates_sm103.cuh",
+                                          "paged_sched_sm103.cuh", "paged_rows_sm103.cuh",
+                                          "paged_tiles_sm103.cuh", "paged_api.cuh", "unit_rates_sm103.cuh",
                                           "sm103_ptx.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 OUT = os.path.join(PKG, "libattn.so")

@@ -23,6 +23,7 @@
 #include "paged_rows_sm103.cuh"
 #include "paged_sched_sm103.cuh"
 #include "paged_tables_sm103.cuh"
+#include "paged_tiles_sm103.cuh"
 #include "unit_rates_sm103.cuh"
 
 namespace {

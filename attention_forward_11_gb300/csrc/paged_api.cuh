@@ -56,6 +56,12 @@ bool opt_in_smem_rows_all() {
     else return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() && opt_in_smem_rows<kF16, kD, 4>();
 }
 
+template <bool kF16, int kD>
+bool opt_in_smem_tiles() {
+    return cudaFuncSetAttribute(attn::paged::paged_tiles_kernel<kF16, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                attn::paged::TilesGeo<kD>::kSmemBytes) == cudaSuccess;
+}
+
 bool paged_device_setup(int dev, int* sm_count) {
     static std::mutex mu;
     static int sms[kMaxDevices] = {};
@@ -65,7 +71,8 @@ bool paged_device_setup(int dev, int* sm_count) {
         int n = 0;
         if (!opt_in_smem_rows_all<false, 64>() || !opt_in_smem_rows_all<true, 64>() ||
             !opt_in_smem_rows_all<false, 128>() || !opt_in_smem_rows_all<true, 128>() ||
-            !opt_in_smem_rows_all<false, 256>() || !opt_in_smem_rows_all<true, 256>() ||
+            !opt_in_smem_tiles<false, 64>() || !opt_in_smem_tiles<true, 64>() || !opt_in_smem_tiles<false, 128>() ||
+            !opt_in_smem_tiles<true, 128>() || !opt_in_smem_rows_all<false, 256>() || !opt_in_smem_rows_all<true, 256>() ||
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
             return false;
         sms[dev] = n;
@@ -125,9 +132,63 @@ attn_status_t launch_rows(const attn::paged::PagedParams& p, void* workspace, in
     return launch_behind(paged_combine_kernel<kF16, kD, G::kRows, 1, 1>, dim3(sms, G::kRows), kCombineThreads, stream, p, sp);
 }
 
+// Does a call take the tcgen05 kernel?  From more than 32 rows a key/value head on (what
+// the rows kernel computes together), where pages can be gathered in boxes of 16 rows or
+// more and the head size has a kernel.
+bool takes_tiles(long long rows, int D, int page_size) { return rows > 32 && D <= 128 && page_size % 16 == 0; }
+
+size_t paged_workspace_bytes(int sms, long long rows, int D, int page_size) {
+    return attn::paged::ws_bytes(sms, takes_tiles(rows, D, page_size) ? attn::kTiles * attn::kBM : 8 * row_blocks_for(rows, D), D);
+}
+
+template <bool kF16, int kD>
+attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, int sms, cudaStream_t stream) {
+    using namespace attn::paged;
+    using T = TilesGeo<kD>;
+    EncodeTiledFn fn = encoder();
+    if (!fn) return ATTN_ERR_CUDA;
+    SchedParams sp{};
+    sp.map = make_row_map(p.Hkv, p.group, attn::kBM, attn::kTiles);
+    sp.ws = split_workspace(workspace, sms, T::kRows);
+    TilesParams tp{};
+    tp.box_rows = 16;
+    while (tp.box_rows < attn::kBN && p.page_size % (2 * tp.box_rows) == 0) tp.box_rows *= 2;
+    tp.tile_tokens = sp.map.tokens / attn::kTiles;
+    tp.q_rows = sp.map.heads * tp.tile_tokens;
+    tp.poll_limit = kDefaultPollLimit;
+    const CUtensorMapDataType type = kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapL2promotion promotion =
+        kD == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUtensorMap tm[3];
+    const cuuint64_t q_dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.Hq, (cuuint64_t)p.total_q};
+    const cuuint64_t q_strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)sp.map.heads, (cuuint32_t)tp.tile_tokens};
+    if (fn(&tm[0], type, 3, const_cast<uint16_t*>(p.q), q_dims, q_strides, q_box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return ATTN_ERR_CUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)p.Hkv, (cuuint64_t)p.page_size, (cuuint64_t)p.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.head_stride * 2, (cuuint64_t)p.token_stride * 2,
+                                   (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)tp.box_rows, 1};
+    for (int i = 0; i < 2; ++i)
+        if (fn(&tm[1 + i], type, 4, const_cast<uint16_t*>(i ? p.v : p.k), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return ATTN_ERR_CUDA;
+    paged_tiles_kernel<kF16, kD><<<sms, attn::kThreads, T::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], p, sp, tp);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles, 8>, dim3(sms, T::kRows / 8),
+                         kCombineThreads, stream, p, sp);
+}
+
 template <bool kF16, int kD>
 attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
-    const int nb = row_blocks_for((long long)max_q_len * p.group, kD);
+    const long long rows = (long long)max_q_len * p.group;
+    if constexpr (kD != 256)
+        if (takes_tiles(rows, kD, p.page_size)) return launch_tiles<kF16, kD>(p, workspace, sms, stream);
+    const int nb = row_blocks_for(rows, kD);
     if (nb == 1) return launch_rows<kF16, kD, 1>(p, workspace, sms, stream);
     if constexpr (kD != 256)
         if (nb == 4) return launch_rows<kF16, kD, 4>(p, workspace, sms, stream);
@@ -242,7 +303,7 @@ extern "C" attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_le
     if ((long long)total_q * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
-    *bytes = attn::paged::ws_bytes(sms, 8 * row_blocks_for((long long)max_q_len * (Hq / Hkv), D), D);
+    *bytes = paged_workspace_bytes(sms, (long long)max_q_len * (Hq / Hkv), D, page_size);
     return ATTN_OK;
 }
 

@@ -315,10 +315,11 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         const float use = M == -INFINITY ? 0.f : M;
-        for (int i0 = part; i0 < h.n; i0 += 4 * kWarpsPer) {
-            float f[4], v[4][kPer];
+        constexpr int kFly = kD == 256 ? 4 : 8;  // pieces in flight
+        for (int i0 = part; i0 < h.n; i0 += kFly * kWarpsPer) {
+            float f[kFly], v[kFly][kPer];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // four pieces in flight
+            for (int j = 0; j < kFly; ++j) {
                 const int i = i0 + j * kWarpsPer;
                 const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
                 f[j] = 0.f;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kFly; ++j)
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) acc[e] += v[j][e] * f[j];
         }
