@@ -289,83 +289,105 @@ def attn_bwd(q, k, v, o, lse, do, causal: int = 0, scale: float | None = None, d
 
 # ---- paged key/value cache
 
-def _paged_call(tensors, stream):
-    """(device, stream handle) of a call on `tensors`, which are all on one GPU.
-    A stream handle of another device's current stream is never taken."""
-    device = tensors[0].device
+# A step of a server makes dozens of these calls, some of a few microseconds on the GPU, so
+# the checks read each property once and nothing is allocated that the caller passed.
+
+def _on_one_gpu(tensors) -> int:
+    """Index of the CUDA device that holds all of `tensors` (None entries aside)."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.device != device or not t.is_cuda):
-            raise AttnError(ATTN_ERR_INVALID_ARG, "all tensors must be on one CUDA device")
-    if stream is None:
-        import torch
-        return device, torch.cuda.current_stream(device).cuda_stream
-    return device, _stream_handle(stream)
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "all tensors must be on one CUDA device")
+    return device
 
 
 class _on:
     """Makes `device` current and, for a stream the caller passed, allocates on that
-    stream, so that memory freed after the call is reused in its order."""
+    stream, so that memory freed after the call is reused in its order.  Yields the
+    stream's handle."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device: int, stream):
         import torch
         self.guards = []
-        if torch.cuda.current_device() != device.index:
+        if torch.cuda.current_device() != device:
             self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            self.guards.append(torch.cuda.stream(s))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", device))
+            self.handle = stream.cuda_stream
+            self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
-def _need(name, t, dtype, shape=None):
-    if t.dtype != dtype or (shape is not None and tuple(t.shape) != shape) or not t.is_contiguous():
-        want = "" if shape is None else f" of shape {shape}"
-        raise AttnError(ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor{want}")
-
-
-def _check_table(table, n_seqs):
+def _is_here(device: int, stream) -> bool:
+    """The common case, for which no guard is set up: the current device and stream."""
     import torch
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seqs or table.stride(1) != 1:
-        raise AttnError(ATTN_ERR_INVALID_ARG, "block_table must be int32 [n_seqs, max_pages] with contiguous rows")
+    return stream is None and torch.cuda.current_device() == device
+
+
+def _current_handle(device: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)  # current_stream(device).cuda_stream, 2 us cheaper
+
+
+def _bad(name, want):
+    raise AttnError(ATTN_ERR_INVALID_ARG, f"{name} must be {want}")
+
+
+def _check_ints(name, t, dtype, n):
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _bad(name, f"a contiguous {dtype} tensor of {n}")
+
+
+def _table_stride(table, n_seqs, i32):
+    if table.dtype is not i32 or table.dim() != 2 or table.shape[0] != n_seqs or table.stride(1) != 1:
+        _bad("block_table", "int32 [n_seqs, max_pages] with contiguous rows")
     return table.stride(0) if n_seqs > 1 else table.shape[1]
 
 
-def _check_cache(k_cache, v_cache):
+def _check_cache(k_cache, v_cache, what, dtype, types):
+    if dtype not in types or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        _bad(f"{what} and the cache", "bf16 or float16, all one type")
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or \
-            k_cache.dtype != v_cache.dtype or k_cache.stride(3) != 1:
-        raise AttnError(ATTN_ERR_INVALID_ARG,
-                        "k_cache and v_cache must be [n_pages, page_size, Hkv, D] of one type, shape and strides, "
-                        "D contiguous")
+            k_cache.stride(3) != 1:
+        _bad("k_cache and v_cache", "[n_pages, page_size, Hkv, D] of one shape and strides, D contiguous")
 
 
 def _row_stride(name, t, heads, D):
     """Row stride of [T, heads, D] with contiguous heads (a slice of a wider row is fine)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != D):
-        raise AttnError(ATTN_ERR_INVALID_ARG, f"{name} must be [T, {heads}, {D}] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    if t.dim() == 3:
+        T, h, d = t.shape
+        row, head, one = t.stride()
+        if h == heads and d == D and one == 1 and (head == D or heads == 1):
+            return row if T > 1 else heads * D
+    _bad(name, f"[T, {heads}, {D}] with contiguous heads")
 
 
 def attn_paged_tables_ptr(*args) -> int:
     """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
-    return int(load_library().attn_paged_tables(*args))
+    return (_lib or load_library()).attn_paged_tables(*args)
 
 
 def attn_paged_append_ptr(*args) -> int:
     """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
-    return int(load_library().attn_paged_append(*args))
+    return (_lib or load_library()).attn_paged_append(*args)
 
 
 def attn_paged_fwd_ptr(*args) -> int:
     """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
-    return int(load_library().attn_paged_fwd(*args))
+    return (_lib or load_library()).attn_paged_fwd(*args)
 
 
 def attn_paged_tables(ctx_lens, new_lens, free_pages, block_table, page_size: int, max_tokens: int, free_head=None,
@@ -380,33 +402,46 @@ def attn_paged_tables(ctx_lens, new_lens, free_pages, block_table, page_size: in
     sequences longer than a table row).  Outputs are allocated here if None.
     """
     import torch
-    n = ctx_lens.shape[0]
-    device, handle = _paged_call((ctx_lens, new_lens, free_pages, block_table, free_head, cu_new, kv_lens, slot_map,
-                                  counts), stream)
+    device = _on_one_gpu((ctx_lens, new_lens, free_pages, block_table, free_head, cu_new, kv_lens, slot_map, counts))
+    if not _is_here(device, stream):
+        with _on(device, stream) as handle:
+            return _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens,
+                                 free_head, cu_new, kv_lens, slot_map, counts)
+    return _paged_tables(torch, _current_handle(device), ctx_lens, new_lens, free_pages, block_table, page_size,
+                         max_tokens, free_head, cu_new, kv_lens, slot_map, counts)
+
+
+def _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_head, cu_new,
+                  kv_lens, slot_map, counts):
     i32 = torch.int32
-    _need("ctx_lens", ctx_lens, i32, (n,))
-    _need("new_lens", new_lens, i32, (n,))
-    _need("free_pages", free_pages, i32, (free_pages.numel(),))
+    n, n_free, max_tokens = ctx_lens.numel(), free_pages.numel(), int(max_tokens)
+    _check_ints("ctx_lens", ctx_lens, i32, n)
+    _check_ints("new_lens", new_lens, i32, n)
+    _check_ints("free_pages", free_pages, i32, n_free)
     if free_head is not None:
-        _need("free_head", free_head, i32, (1,))
-    table_stride = _check_table(block_table, n)
-    with _on(device, stream):
-        if cu_new is None:
-            cu_new = torch.empty(n + 1, dtype=i32, device=device)
-        if kv_lens is None:
-            kv_lens = torch.empty(n, dtype=i32, device=device)
-        if slot_map is None:
-            slot_map = torch.empty(max_tokens, dtype=torch.int64, device=device)
-        if counts is None:
-            counts = torch.empty(4, dtype=i32, device=device)
-        _need("cu_new", cu_new, i32, (n + 1,))
-        _need("kv_lens", kv_lens, i32, (n,))
-        _need("slot_map", slot_map, torch.int64, (max_tokens,))
-        _need("counts", counts, i32, (4,))
-        st = attn_paged_tables_ptr(ctx_lens.data_ptr(), new_lens.data_ptr(), n, int(page_size), free_pages.data_ptr(),
-                                   free_pages.numel(), 0 if free_head is None else free_head.data_ptr(),
-                                   block_table.data_ptr(), block_table.shape[1], table_stride, cu_new.data_ptr(),
-                                   kv_lens.data_ptr(), slot_map.data_ptr(), int(max_tokens), counts.data_ptr(), handle)
+        _check_ints("free_head", free_head, i32, 1)
+    table_stride = _table_stride(block_table, n, i32)
+    device = ctx_lens.device
+    if cu_new is None:
+        cu_new = torch.empty(n + 1, dtype=i32, device=device)
+    else:
+        _check_ints("cu_new", cu_new, i32, n + 1)
+    if kv_lens is None:
+        kv_lens = torch.empty(n, dtype=i32, device=device)
+    else:
+        _check_ints("kv_lens", kv_lens, i32, n)
+    if slot_map is None:
+        slot_map = torch.empty(max(max_tokens, 0), dtype=torch.int64, device=device)
+    else:
+        _check_ints("slot_map", slot_map, torch.int64, max_tokens)
+    if counts is None:
+        counts = torch.empty(4, dtype=i32, device=device)
+    else:
+        _check_ints("counts", counts, i32, 4)
+    st = attn_paged_tables_ptr(ctx_lens.data_ptr(), new_lens.data_ptr(), n, page_size, free_pages.data_ptr(), n_free,
+                               0 if free_head is None else free_head.data_ptr(), block_table.data_ptr(),
+                               block_table.shape[1], table_stride, cu_new.data_ptr(), kv_lens.data_ptr(),
+                               slot_map.data_ptr(), max_tokens, counts.data_ptr(), handle)
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_tables")
     return cu_new, kv_lens, slot_map, counts
@@ -417,20 +452,21 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
     slots slot_map[t] (int64 [T], rows outside the cache skipped) of k_cache and v_cache
     ([n_pages, page_size, Hkv, D], any strides with D contiguous), in place."""
     import torch
-    device, handle = _paged_call((k, v, slot_map, k_cache, v_cache), stream)
-    _check_cache(k_cache, v_cache)
+    device = _on_one_gpu((k, v, slot_map, k_cache, v_cache))
+    _check_cache(k_cache, v_cache, "k, v", k.dtype, (torch.bfloat16, torch.float16))
     n_pages, page_size, Hkv, D = k_cache.shape
-    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype or k.dtype not in (torch.bfloat16, torch.float16):
-        raise AttnError(ATTN_ERR_INVALID_ARG, "k, v and the cache must be bf16 or float16, all one type")
-    _need("slot_map", slot_map, torch.int64, (k.shape[0],))
-    if v.shape[0] != k.shape[0]:
-        raise AttnError(ATTN_ERR_INVALID_ARG, "k and v must have the same number of rows")
-    ks, vs = _row_stride("k", k, Hkv, D), _row_stride("v", v, Hkv, D)
+    T = k.shape[0]
+    if v.dtype is not k.dtype or v.shape[0] != T:
+        _bad("v", "of k's type, with as many rows")
+    _check_ints("slot_map", slot_map, torch.int64, T)
     ps, ts, hs, _ = k_cache.stride()
-    with _on(device, stream):
-        st = attn_paged_append_ptr(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
-                                   v_cache.data_ptr(), k.shape[0], Hkv, D, n_pages, page_size, ks, vs, ps, ts, hs,
-                                   handle)
+    args = (k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, D, n_pages,
+            page_size, _row_stride("k", k, Hkv, D), _row_stride("v", v, Hkv, D), ps, ts, hs)
+    if _is_here(device, stream):
+        st = attn_paged_append_ptr(*args, _current_handle(device))
+    else:
+        with _on(device, stream) as handle:
+            st = attn_paged_append_ptr(*args, handle)
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")
 
@@ -458,41 +494,49 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: i
     attn_paged_fwd_workspace_size(...) bytes; it and the outputs are allocated here if None.
     """
     import torch
-    device, handle = _paged_call((q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse, workspace), stream)
-    _check_cache(k_cache, v_cache)
+    device = _on_one_gpu((q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse, workspace))
+    if not _is_here(device, stream):
+        with _on(device, stream) as handle:
+            return _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o,
+                              lse, workspace, want_lse)
+    return _paged_fwd(torch, _current_handle(device), q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal,
+                      scale, o, lse, workspace, want_lse)
+
+
+def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o, lse, workspace,
+               want_lse):
+    dtype, i32 = q.dtype, torch.int32
+    _check_cache(k_cache, v_cache, "q", dtype, (torch.bfloat16, torch.float16))
     n_pages, page_size, Hkv, D = k_cache.shape
-    if q.dtype not in (torch.bfloat16, torch.float16) or k_cache.dtype != q.dtype:
-        raise AttnError(ATTN_ERR_INVALID_ARG, "q and the cache must be bf16 or float16, all one type")
-    T, Hq = q.shape[0], q.shape[1]
+    n = kv_lens.numel()
+    _check_ints("kv_lens", kv_lens, i32, n)
+    _check_ints("cu_q", cu_q, i32, n + 1)
+    if q.dim() != 3:
+        _bad("q", "[T, Hq, D]")
+    T, Hq, _ = q.shape
     q_stride = _row_stride("q", q, Hq, D)
-    n = kv_lens.shape[0]
-    _need("kv_lens", kv_lens, torch.int32, (n,))
-    _need("cu_q", cu_q, torch.int32, (n + 1,))
-    table_stride = _check_table(block_table, n)
+    table_stride = _table_stride(block_table, n, i32)
     ps, ts, hs, _ = k_cache.stride()
-    with _on(device, stream):
-        if o is None:
-            o = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
-        _need("o", o, q.dtype, (T, Hq, D))
-        if lse is None and want_lse:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
-        if lse is not None:
-            _need("lse", lse, torch.float32, (Hq, T))
-        if scale is None:
-            scale = 1.0 / (D ** 0.5)
-        if max_q_len is None:
-            max_q_len = T
-        if workspace is None:
-            size = attn_paged_fwd_workspace_size(T, max_q_len, Hq, Hkv, D, page_size)
-            if size:
-                workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        st = attn_paged_fwd_ptr(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-                                0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                                kv_lens.data_ptr(), n, T, int(max_q_len), Hq, Hkv, D, n_pages, page_size,
-                                block_table.shape[1], q_stride, table_stride, ps, ts, hs, int(causal), float(scale),
-                                ATTN_DTYPE_F16 if q.dtype == torch.float16 else ATTN_DTYPE_BF16,
-                                0 if workspace is None else workspace.data_ptr(),
-                                0 if workspace is None else workspace.numel() * workspace.element_size(), handle)
+    if o is None:
+        o = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+    elif o.dtype is not dtype or tuple(o.shape) != (T, Hq, D) or not o.is_contiguous():
+        _bad("o", "a contiguous [T, Hq, D] tensor of q's type")
+    if lse is not None:
+        if lse.dtype is not torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+            _bad("lse", "a contiguous float32 [Hq, T] tensor")
+    elif want_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if max_q_len is None:
+        max_q_len = T
+    if workspace is None:
+        size = attn_paged_fwd_workspace_size(T, max_q_len, Hq, Hkv, D, page_size)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    st = attn_paged_fwd_ptr(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                            0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                            kv_lens.data_ptr(), n, T, max_q_len, Hq, Hkv, D, n_pages, page_size, block_table.shape[1],
+                            q_stride, table_stride, ps, ts, hs, causal, D ** -0.5 if scale is None else scale,
+                            ATTN_DTYPE_F16 if dtype is torch.float16 else ATTN_DTYPE_BF16, workspace.data_ptr(),
+                            workspace.nbytes, handle)
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_fwd")
     return o, lse

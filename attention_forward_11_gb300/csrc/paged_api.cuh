@@ -329,24 +329,24 @@ extern "C" attn_status_t attn_paged_fwd(const void* q, const void* k_cache, cons
     for (const void* ptr : {(const void*)lse, (const void*)block_table, (const void*)cu_q, (const void*)kv_lens})
         if (!aligned(ptr, 4)) return ATTN_ERR_INVALID_ARG;
     if (workspace && !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
-    size_t need = 0;
-    const attn_status_t sw = attn_paged_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, &need);
-    if (sw != ATTN_OK) return sw;
-    if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+    if ((long long)total_q * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     // o, lse and the workspace overlap no input and not each other
     const size_t cache = cache_extent(n_pages, page_size, Hkv, D, page_stride, token_stride, head_stride);
-    const void* out_p[3] = {o, lse, workspace};
-    const size_t out_n[3] = {(size_t)total_q * row * 2, lse ? (size_t)total_q * Hq * 4 : 0, need};
-    const void* in_p[6] = {q, k_cache, v_cache, block_table, cu_q, kv_lens};
-    const size_t in_n[6] = {((size_t)(total_q - 1) * q_stride + row) * 2, cache, cache,
-                            ((size_t)(n_seqs - 1) * table_stride + max_pages) * 4, ((size_t)n_seqs + 1) * 4, (size_t)n_seqs * 4};
-    for (int a = 0; a < 3; ++a) {
-        if (out_n[a] == 0) continue;
-        for (int c = 0; c < 6; ++c)
-            if (ranges_overlap(out_p[a], out_n[a], in_p[c], in_n[c])) return ATTN_ERR_INVALID_ARG;
-        for (int c = a + 1; c < 3; ++c)
-            if (out_n[c] > 0 && ranges_overlap(out_p[a], out_n[a], out_p[c], out_n[c])) return ATTN_ERR_INVALID_ARG;
-    }
+    const void* in_p[8] = {q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse};
+    const size_t o_bytes = (size_t)total_q * row * 2, lse_bytes = lse ? (size_t)total_q * Hq * 4 : 0;
+    const size_t in_n[8] = {((size_t)(total_q - 1) * q_stride + row) * 2, cache, cache,
+                            ((size_t)(n_seqs - 1) * table_stride + max_pages) * 4, ((size_t)n_seqs + 1) * 4,
+                            (size_t)n_seqs * 4, o_bytes, lse_bytes};
+    for (int c = 0; c < 6; ++c)
+        if (ranges_overlap(o, o_bytes, in_p[c], in_n[c]) || (lse && ranges_overlap(lse, lse_bytes, in_p[c], in_n[c])))
+            return ATTN_ERR_INVALID_ARG;
+    if (lse && ranges_overlap(lse, lse_bytes, o, o_bytes)) return ATTN_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
+    const size_t need = paged_workspace_bytes(sms, (long long)max_q_len * (Hq / Hkv), D, page_size);
+    if (!workspace || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+    for (int c = 0; c < 8; ++c)
+        if (in_n[c] > 0 && ranges_overlap(workspace, need, in_p[c], in_n[c])) return ATTN_ERR_INVALID_ARG;
     attn::paged::PagedParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.k = static_cast<const uint16_t*>(k_cache);
@@ -374,8 +374,6 @@ extern "C" attn_status_t attn_paged_fwd(const void* q, const void* k_cache, cons
     p.head_stride = head_stride;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || !paged_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
     const bool f16 = dtype == ATTN_DTYPE_F16;
     if (D == 64) return f16 ? launch_paged<true, 64>(p, max_q_len, workspace, sms, stream) : launch_paged<false, 64>(p, max_q_len, workspace, sms, stream);
     if (D == 128) return f16 ? launch_paged<true, 128>(p, max_q_len, workspace, sms, stream) : launch_paged<false, 128>(p, max_q_len, workspace, sms, stream);

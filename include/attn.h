@@ -289,9 +289,11 @@ attn_status_t attn_paged_append(const void* k, const void* v, const long long* s
  *              finite.
  * Hq, Hkv, D, scale, dtype  as attn_fwd_ex.
  * workspace    device pointer, 256-byte aligned, of at least
- *              attn_paged_fwd_workspace_size bytes for the current device, or NULL when
- *              that is 0.  Scratch: its contents are undefined before and after the
- *              call, and calls that overlap in time on the GPU must not share one.
+ *              attn_paged_fwd_workspace_size bytes for the current device (the size for
+ *              the same total_q .. page_size).  Scratch: its contents are undefined before
+ *              and after the call, and calls that overlap in time on the GPU must not
+ *              share one.
+ * total_q * Hq is at most 2^31 - 1.
  *
  * Arithmetic as attn_fwd: operands and P in the element type, products and softmax
  * statistics in fp32, O rounded to nearest even once.  Results do not depend on timing:
