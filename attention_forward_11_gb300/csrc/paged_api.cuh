@@ -53,7 +53,8 @@ bool opt_in_smem_rows() {
 template <bool kF16, int kD>
 bool opt_in_smem_rows_all() {
     if constexpr (kD == 256) return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>();
-    else return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() && opt_in_smem_rows<kF16, kD, 4>();
+    else return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() &&
+                opt_in_smem_rows<kF16, kD, 3>() && opt_in_smem_rows<kF16, kD, 4>();
 }
 
 template <bool kF16, int kD>
@@ -92,25 +93,34 @@ attn::paged::Workspace split_workspace(void* workspace, int sms, int rows) {
     return w;
 }
 
+// The tag of a launch that counts its pieces in a workspace of unknown contents: 48 bits
+// of a product, so that they look like nothing a buffer is likely to hold.
+unsigned long long next_tag() {
+    static std::atomic<unsigned long long> launches{0};
+    const unsigned long long tag = (launches.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull >> 16;
+    return tag != 0 ? tag : 1;
+}
+
 // 8-row blocks of the rows kernel for sequences of at most `rows` (token, head) rows a
 // key/value head.  At head size 256 four blocks' sums do not fit the registers.
-int row_blocks_for(long long rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
+int row_blocks_for(long long rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : rows <= 24 ? 3 : 4; }
 
-// Launched so that its blocks are in place while the first kernel's still run; they wait
-// for its end before they read.
-template <class Kernel>
-attn_status_t launch_behind(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, const attn::paged::PagedParams& p,
-                            const attn::paged::SchedParams& sp) {
+// Launched so that its blocks are in place while the kernel before it in the stream still
+// runs (if that one allows it); they wait for its end before they read or write anything.
+template <class... Params, class... Args>
+attn_status_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                            const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, p, sp) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
         (void)cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
@@ -125,11 +135,8 @@ attn_status_t launch_rows(const attn::paged::PagedParams& p, void* workspace, in
     SchedParams sp{};
     sp.map = make_row_map(p.Hkv, p.group, G::kRows, 1);
     sp.ws = split_workspace(workspace, sms, G::kRows);
-    paged_rows_kernel<kF16, kD, kNB><<<sms, G::kThreads, G::kSmemBytes, stream>>>(p, sp);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    // one row a block: a long sequence alone has as many pieces as there are SMs
-    return launch_behind(paged_combine_kernel<kF16, kD, G::kRows, 1, 1>, dim3(sms, G::kRows), kCombineThreads, stream, p, sp);
+    sp.tag = next_tag();
+    return launch_behind(paged_rows_kernel<kF16, kD, kNB>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
 }
 
 // Does a call take the tcgen05 kernel?  From more than 32 rows a key/value head on (what
@@ -176,11 +183,11 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return ATTN_ERR_CUDA;
-    paged_tiles_kernel<kF16, kD><<<sms, attn::kThreads, T::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], p, sp, tp);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    g_launches.fetch_add(1, std::memory_order_relaxed);
+    const attn_status_t st = launch_behind(paged_tiles_kernel<kF16, kD>, dim3(sms), attn::kThreads, T::kSmemBytes, stream,
+                                           tm[0], tm[1], tm[2], p, sp, tp);
+    if (st != ATTN_OK) return st;
     return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles, 8>, dim3(sms, T::kRows / 8),
-                         kCombineThreads, stream, p, sp);
+                         kCombineThreads, 0, stream, p, sp);
 }
 
 template <bool kF16, int kD>
@@ -190,8 +197,10 @@ attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, voi
         if (takes_tiles(rows, kD, p.page_size)) return launch_tiles<kF16, kD>(p, workspace, sms, stream);
     const int nb = row_blocks_for(rows, kD);
     if (nb == 1) return launch_rows<kF16, kD, 1>(p, workspace, sms, stream);
-    if constexpr (kD != 256)
+    if constexpr (kD != 256) {
+        if (nb == 3) return launch_rows<kF16, kD, 3>(p, workspace, sms, stream);
         if (nb == 4) return launch_rows<kF16, kD, 4>(p, workspace, sms, stream);
+    }
     return launch_rows<kF16, kD, 2>(p, workspace, sms, stream);
 }
 
@@ -239,10 +248,7 @@ extern "C" attn_status_t attn_paged_tables(const int* ctx_lens, const int* new_l
     p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
     // one block per 1024 tokens, at most 128: each repeats the scan over the sequences
     const int blocks = std::min(128, (max_tokens + attn::paged::kTableThreads - 1) / attn::paged::kTableThreads);
-    attn::paged::paged_tables_kernel<<<blocks, attn::paged::kTableThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return ATTN_OK;
+    return launch_behind(attn::paged::paged_tables_kernel, dim3(blocks), attn::paged::kTableThreads, 0, stream, p);
 }
 
 extern "C" attn_status_t attn_paged_append(const void* k, const void* v, const long long* slot_map, void* k_cache,
@@ -288,10 +294,7 @@ extern "C" attn_status_t attn_paged_append(const void* k, const void* v, const l
     p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
     p.by_row = attn::paged::make_fastdiv(static_cast<unsigned int>(p.row_chunks));
     const unsigned int blocks = static_cast<unsigned int>(((long long)n_tokens + p.per_block - 1) / p.per_block);
-    attn::paged::paged_append_kernel<<<blocks, attn::paged::kAppendThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return ATTN_OK;
+    return launch_behind(attn::paged::paged_append_kernel, dim3(blocks), attn::paged::kAppendThreads, 0, stream, p);
 }
 
 extern "C" attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,

@@ -60,5 +60,19 @@ __device__ __forceinline__ int visible_keys(const PagedParams& p, const Seq& x, 
     return p.causal ? max(x.kv_len - x.q_len + t + 1, 0) : x.kv_len;
 }
 
+// Programmatic launch: a kernel's blocks may be in place before the kernel in front of it
+// has ended; every thread waits for that end before it touches memory.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Reads a word of every 64 bytes of a kernel's parameters, whose first reads miss one after
+// another otherwise (a block calls it before it waits for the kernel in front).
+template <class P>
+__device__ __forceinline__ void touch_params(const P& p) {
+    const int* w = reinterpret_cast<const int*>(&p);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(P) / 4); i += 16) asm volatile("" ::"r"(w[i]));
+}
+
 }  // namespace paged
 }  // namespace attn

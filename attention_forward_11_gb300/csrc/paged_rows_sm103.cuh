@@ -14,10 +14,11 @@
 // their (m, l, O) are merged in a fixed order.  P is rounded to the operands' type for
 // its product, as in the dense forward.
 //
-// One block a SM takes an equal share of the batch (paged_sched_sm103.cuh).  Each warp
-// fills a ring of its own with cp.async, kStages - 1 slices ahead of the one it computes
-// and across the ends of units, with no barrier between warps: 16-byte copies follow any
-// page size and any strides, and a slice's page numbers are read one slice earlier still.
+// One block a SM takes an equal share of the batch (paged_sched_sm103.cuh); of the blocks
+// that have a piece of one unit, the last to finish joins them.  Each warp
+// fills a ring of its own with cp.async, two slices ahead of the one it computes and across
+// the ends of units, with no barrier between warps: 16-byte copies follow any page size and
+// any strides, and a slice's page numbers are read one slice earlier still.
 #pragma once
 #include <cmath>
 #include <cstdint>
@@ -81,10 +82,12 @@ struct RowsGeo {
     static constexpr int kWarps = kD == 256 ? 4 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * kNB;
-    static constexpr int kTileKeys = 16 * kWarps;       // keys of all warps in one step
-    static constexpr int kSliceBytes = 16 * kD * 2;     // K or V rows of one warp's step
+    static constexpr int kKS = kD == 64 ? 2 : 1;        // 16-key blocks of a warp's slice
+    static constexpr int kSlice = 16 * kKS;             // keys of a slice
+    static constexpr int kTileKeys = kSlice * kWarps;   // keys of all warps in one step
+    static constexpr int kSliceBytes = kSlice * kD * 2; // K or V rows of a slice
     static constexpr int kChunks = kD / 8;              // 16-byte pieces of a row
-    static constexpr int kStages = kD == 64 ? 6 : 3;    // 192 KB of slices
+    static constexpr int kStages = 3;                   // 192 KB of slices
     static constexpr int kMergeCols = 64;               // columns of O merged at a time
     static constexpr int kMergeStride = kMergeCols + 4; // floats; rows 2 t of a warp fall into different banks
     static constexpr int kRing = kWarps * kStages * 2 * kSliceBytes;
@@ -92,60 +95,162 @@ struct RowsGeo {
     static constexpr int kStats = kWarps * kRows * 8;
     static constexpr int kSmemBytes = kRing + kMerge + kStats;
     static_assert(kSmemBytes <= 231000, "ring, merge buffer and static shared memory exceed 227 KB");
-    // a piece is worth its merge from two tiles on, a share from four
-    static constexpr int kMinPiece = 2, kMinShare = 4;
+    static_assert(kMerge >= kThreads / (kD / 4) * (kD + 4) * 4, "joined rows do not fit the merge buffer");
+    // a piece is worth its merge from two tiles on; cutting a unit costs its end some 4 us,
+    // which is the time of eight tiles when few blocks read
+    static constexpr int kMinPiece = 2, kMinShare = 8;
     using ShareT = Share<kTileKeys, kMinPiece, kMinShare>;
     using CursorT = Cursor<ShareT, kTileKeys>;
 };
+
+// Joins the n pieces of a unit that block `first` started: M = max m, L = sum l 2^(m - M),
+// O = sum O 2^(m - M) / L.  kD / 4 threads have a row (four columns each), or, when there are
+// fewer rows than such groups, a part of a row's pieces; `buf` is shared scratch of a row and
+// its sum for every group.  A block does this alone at its end, so what counts is how many
+// loads wait on one another: 16 pieces are in flight at once, the first before M is known.
+template <bool kF16, int kD, int kRows, int kThreads>
+__device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedParams& sp, const Seq& x, int head_unit, int t0,
+                                            int first, int n, float* buf) {
+    constexpr int kLanes = kD / 4, kGroups = kThreads / kLanes, kFly = 16;
+    constexpr int kSpan = kLanes < 32 ? kLanes : 32;  // lanes that share a search for M
+    const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4, lane = threadIdx.x % kSpan;
+    const int rows = min(min(sp.map.tokens, x.q_len - t0) * sp.map.heads, kRows);
+    int parts = 1;
+    while (2 * parts * rows <= kGroups) parts *= 2;
+    const int part = group % parts;
+    for (int r0 = 0; r0 < rows; r0 += kGroups / parts) {
+        const int r = min(r0 + group / parts, kRows - 1);  // rows past the last are computed and not stored
+        const Row w = row_of(p, sp.map, x, head_unit, t0, sp.map.tokens, r);
+        const bool mine = r0 + group / parts < rows && w.there;
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = part; i0 == part || i0 < n; i0 += kFly * parts) {  // the first step is every thread's
+            float2 ml[kFly];
+            float4 v[kFly];
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                const int i = i0 + j * parts;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mine && i < n) {
+                    const size_t row = (size_t)piece_slot(first, i) * kRows + r;
+                    ml[j] = __ldcg(sp.ws.ml + row);
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(sp.ws.o + row * kD + col));
+                }
+            }
+            if (i0 == part) {
+                for (int i = lane; mine && i < n; i += kSpan)
+                    M = fmaxf(M, __ldcg(sp.ws.ml + (size_t)piece_slot(first, i) * kRows + r).x);
+#pragma unroll
+                for (int d = kSpan / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            }
+            const float use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                const float f = ex2_approx(ml[j].x - use);
+                L += ml[j].y * f;
+                acc.x += v[j].x * f;
+                acc.y += v[j].y * f;
+                acc.z += v[j].z * f;
+                acc.w += v[j].w * f;
+            }
+        }
+        if (parts > 1) {
+            float* to = buf + group * (kD + 4);
+            *reinterpret_cast<float4*>(to + col) = acc;
+            if (col == 0) to[kD] = L;
+            __syncthreads();
+            if (part == 0)
+                for (int k = 1; k < parts; ++k) {
+                    const float* from = buf + (group + k) * (kD + 4);
+                    const float4 y = *reinterpret_cast<const float4*>(from + col);
+                    acc.x += y.x;
+                    acc.y += y.y;
+                    acc.z += y.z;
+                    acc.w += y.w;
+                    L += from[kD];
+                }
+        }
+        if (!mine || part != 0) continue;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const size_t tok = (size_t)x.q0 + w.token;
+        *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
+            make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
+        if (col == 0 && p.lse != nullptr)
+            p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    }
+}
 
 template <bool kF16, int kD, int kNB>
 __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
     paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ SchedParams sp) {
     using G = RowsGeo<kD, kNB>;
+    constexpr int kKS = G::kKS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_part[G::kWarps];
+    __shared__ long long s_part[2 * G::kWarps];
     __shared__ StartPos s_start;
     __shared__ uint32_t s_valid[G::kWarps][G::kStages];  // keys of a slice that have a page
+    __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * (G::kStages * 2 * G::kSliceBytes);
     float* merge = reinterpret_cast<float*>(smem + G::kRing);
     float2* stats = reinterpret_cast<float2*>(smem + G::kRing + G::kMerge);
     launch_dependents();
+    touch_params(p);
+    touch_params(sp);
+    wait_for_primary();
 
     typename G::ShareT sh;
-    if (tid == 0) sp.ws.header[blockIdx.x].n = 0;
     const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare>(p, sp, s_part, &s_start, sh);
     if (!some) return;
     typename G::CursorT cur;
     cur.first(p, sp, sh, s_start);
     typename G::CursorT ld = cur;  // the copies' position, ahead of the products'
     int ld_tile = ld.tile;
+    // the counts of the pieces at this share's ends (ready before any is counted)
+    CountWord counts[2];
+    if (tid == G::kThreads - 1) {
+        counts[0] = look_at_count(sp.ws.count(static_cast<int>(blockIdx.x)));
+        counts[1] = look_at_count(sp.ws.count(cur.ok && cur.tile > 0 ? sh.starter(cur.at) : static_cast<int>(blockIdx.x)));
+    }
 
-    // The page numbers of the next slice to copy: lane i has that of key i % 16.
-    int page = -1, page_row = 0;
-    auto look_up = [&]() {
-        page = -1;
-        if (!ld.ok) return;
-        const int key = ld_tile * G::kTileKeys + 16 * warp + (lane & 15);
-        if (key >= ld.keys) return;
-        const int col = static_cast<int>(p.by_page.quot(key));
-        page = p.table[ld.s * p.table_stride + col];
-        page_row = key - col * p.page_size;
+    // The page numbers of the next slices to copy: lane i has that of key i % kSlice.  A slice
+    // is looked up when the one before it is copied, the first three together.
+    struct Look {
+        int page, row;    // page number and row of this lane's key
+        int hkv;          // key/value head
+        bool some;        // the slice has keys
+        bool ok;          // there is such a slice
     };
-    // Copies that slice into a stage, then moves on.
-    auto issue = [&](int st) {
-        if (ld.ok) {
-            const bool there = page >= 0 && page < p.n_pages;
-            const long long base = there ? page * p.page_stride + page_row * p.token_stride +
-                                               ld.head_unit / sp.map.splits * p.head_stride
-                                         : 0;
-            const uint32_t valid = __ballot_sync(0xffffffffu, there) & 0xffffu;
+    auto look_up = [&](Look& k) {
+        k.page = -1;
+        k.ok = ld.ok;
+        if (!ld.ok) return;
+        const int key = ld_tile * G::kTileKeys + G::kSlice * warp + (lane & (G::kSlice - 1));
+        k.some = ld_tile * G::kTileKeys + G::kSlice * warp < ld.keys;
+        k.hkv = sp.map.kv_head(ld.head_unit);
+        if (key < ld.keys) {
+            const int col = static_cast<int>(p.by_page.quot(key));
+            k.page = p.table[ld.s * p.table_stride + col];
+            k.row = key - col * p.page_size;
+        }
+        if (++ld_tile == ld.tile_end) {
+            ld.next(p, sp, sh);
+            ld_tile = ld.tile;
+        }
+    };
+    // Copies a slice into a stage.
+    auto copy = [&](const Look& k, int st) {
+        if (k.ok) {
+            const bool there = k.page >= 0 && k.page < p.n_pages;
+            const long long base = there ? k.page * p.page_stride + k.row * p.token_stride + k.hkv * p.head_stride : 0;
+            const uint32_t valid = __ballot_sync(0xffffffffu, there);
             if (lane == 0) s_valid[warp][st] = valid;
             const uint32_t to = ring + st * (2 * G::kSliceBytes);
-            if (ld_tile * G::kTileKeys + 16 * warp < ld.keys) {
+            if (k.some) {
 #pragma unroll
-                for (int i = 0; i < G::kChunks / 2; ++i) {
+                for (int i = 0; i < G::kSlice * G::kChunks / 32; ++i) {
                     const int idx = lane + 32 * i, kk = idx / G::kChunks, ch = idx % G::kChunks;
                     const long long at = __shfl_sync(0xffffffffu, base, kk) + ch * 8;
                     const bool ok = (valid >> kk) & 1;
@@ -154,17 +259,23 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
                     cp_async16(dst + G::kSliceBytes, p.v + at, ok);
                 }
             }
-            if (++ld_tile == ld.tile_end) {
-                ld.next(p, sp, sh);
-                ld_tile = ld.tile;
-            }
-            look_up();
         }
         cp_async_commit();
     };
-    look_up();
-#pragma unroll 1
-    for (int st = 0; st < G::kStages; ++st) issue(st);
+    static_assert(G::kStages == 3, "two slices are copied ahead");
+    Look next;
+    {
+        Look k0, k1;
+        look_up(k0);
+        look_up(k1);
+        look_up(next);
+        copy(k0, 0);
+        copy(k1, 1);
+    }
+    if (tid == G::kThreads - 1) {
+        begin_count(counts[0], sp.tag);
+        if (counts[1].word != counts[0].word) begin_count(counts[1], sp.tag);
+    }
     int st = 0;
 
 #pragma unroll 1
@@ -184,17 +295,20 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
             }
         }
         // this thread's two rows of every row block: 2 t4 and 2 t4 + 1
-        int lim[kNB][2];
+        int lim[kNB][2], all_see = 0x7fffffff;  // keys that every row sees
         float m[kNB][2], l[kNB][2], o[kNB][kD / 16][4];
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + 2 * t4 + e);
-                lim[nb][e] = w.there ? visible_keys(p, x, w.token) : 0;
+                lim[nb][e] = w.there ? visible_keys(p, x, w.token) : 0x7fffffff;  // a row that is none masks nothing
+                all_see = min(all_see, lim[nb][e]);
                 m[nb][e] = -INFINITY;
                 l[nb][e] = 0.f;
             }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, d));
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
@@ -204,73 +318,111 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
 
 #pragma unroll 1
         for (int tile = cur.tile; tile < cur.tile_end; ++tile) {
-            cp_async_wait<G::kStages - 1>();
-            __syncwarp();
-            const int k0 = tile * G::kTileKeys + 16 * warp;
+            cp_async_wait<G::kStages - 2>();
+            __syncwarp();  // the slice is there, and every lane is done with the one before
+            copy(next, st == 0 ? G::kStages - 1 : st - 1);
+            look_up(next);
+            const int k0 = tile * G::kTileKeys + G::kSlice * warp;
             const uint32_t from = ring + st * (2 * G::kSliceBytes);
             const uint32_t valid = s_valid[warp][st];
             if (k0 < cur.keys) {
-                float sc[kNB][4];
+                // one product after another would wait for the sum: a single chain is cut in two
+                constexpr bool kTwoSums = kNB * kKS == 1;
+                float sc[kNB][kKS][4], sc2[kNB][kKS][4];
 #pragma unroll
-                for (int nb = 0; nb < kNB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+                for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                    for (int b = 0; b < kKS; ++b) {
+                        sc[nb][b][0] = sc[nb][b][1] = sc[nb][b][2] = sc[nb][b][3] = 0.f;
+                        sc2[nb][b][0] = sc2[nb][b][1] = sc2[nb][b][2] = sc2[nb][b][3] = 0.f;
+                    }
                 {
                     const int kk = (lane & 7) + ((lane >> 3) & 1) * 8;
                     const uint32_t a0 = from + kk * (kD * 2);
 #pragma unroll
-                    for (int ks = 0; ks < kD / 16; ++ks) {
-                        uint32_t a[4];
-                        ldsm_x4(a, a0 + (((2 * ks + (lane >> 4)) ^ (kk & 7)) << 4));
+                    for (int ks = 0; ks < kD / 16; ++ks)
 #pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(sc[nb], a, qf[nb][ks][0], qf[nb][ks][1]);
-                    }
+                        for (int b = 0; b < kKS; ++b) {
+                            uint32_t a[4];
+                            ldsm_x4(a, a0 + b * (16 * kD * 2) + (((2 * ks + (lane >> 4)) ^ (kk & 7)) << 4));
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb)
+                                mma_16816<kF16>(kTwoSums && (ks & 1) ? sc2[nb][b] : sc[nb][b], a, qf[nb][ks][0], qf[nb][ks][1]);
+                        }
+                    if constexpr (kTwoSums)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[0][0][e] += sc2[0][0][e];
                 }
-                uint32_t pf[kNB][2];
+                if (k0 + G::kSlice > all_see || valid != 0xffffffffu) {
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                        for (int b = 0; b < kKS; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int kk = 16 * b + 8 * (e / 2) + g;
+                                if (!((valid >> kk) & 1) || k0 + kk >= lim[nb][e % 2]) sc[nb][b][e] = -INFINITY;
+                            }
+                }
+                uint32_t pf[kNB][kKS][2];
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
-                    // element e of sc: key k0 + g + 8 (e / 2), row 2 t4 + e % 2
+                    // element e of block b: key k0 + 16 b + g + 8 (e / 2), row 2 t4 + e % 2
                     float al[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const bool v0 = ((valid >> g) & 1) && k0 + g < lim[nb][e];
-                        const bool v1 = ((valid >> (g + 8)) & 1) && k0 + g + 8 < lim[nb][e];
-                        float a = v0 ? sc[nb][e] * p.scale_log2 : -INFINITY;
-                        float b = v1 ? sc[nb][e + 2] * p.scale_log2 : -INFINITY;
-                        float mx = fmaxf(a, b);
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int b = 0; b < kKS; ++b)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) mx = fmaxf(mx, sc[nb][b][2 * u + e]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        const float mn = fmaxf(m[nb][e], mx), use = mn == -INFINITY ? 0.f : mn;
+                        const float mn = fmaxf(m[nb][e], mx * p.scale_log2), use = mn == -INFINITY ? 0.f : mn;
                         al[e] = ex2_approx(m[nb][e] - use);
                         m[nb][e] = mn;
-                        a = ex2_approx(a - use);
-                        b = ex2_approx(b - use);
-                        l[nb][e] = l[nb][e] * al[e] + (a + b);
-                        sc[nb][e] = a;
-                        sc[nb][e + 2] = b;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int b = 0; b < kKS; ++b)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float& y = sc[nb][b][2 * u + e];
+                                y = ex2_approx(fmaf(y, p.scale_log2, -use));
+                                sum += y;
+                            }
+                        l[nb][e] = l[nb][e] * al[e] + sum;
+                    }
+                    // the maximum settles after a few slices: most leave O as it is
+                    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+                        for (int mt = 0; mt < kD / 16; ++mt) {
+                            o[nb][mt][0] *= al[0];
+                            o[nb][mt][1] *= al[1];
+                            o[nb][mt][2] *= al[0];
+                            o[nb][mt][3] *= al[1];
+                        }
                     }
 #pragma unroll
-                    for (int mt = 0; mt < kD / 16; ++mt) {
-                        o[nb][mt][0] *= al[0];
-                        o[nb][mt][1] *= al[1];
-                        o[nb][mt][2] *= al[0];
-                        o[nb][mt][3] *= al[1];
+                    for (int b = 0; b < kKS; ++b) {
+                        pf[nb][b][0] = movmatrix(pack_x2<kF16>(sc[nb][b][0], sc[nb][b][1]));
+                        pf[nb][b][1] = movmatrix(pack_x2<kF16>(sc[nb][b][2], sc[nb][b][3]));
                     }
-                    pf[nb][0] = movmatrix(pack_x2<kF16>(sc[nb][0], sc[nb][1]));
-                    pf[nb][1] = movmatrix(pack_x2<kF16>(sc[nb][2], sc[nb][3]));
                 }
                 {
                     const int kk = (lane & 7) + (lane >> 4) * 8;
                     const uint32_t a0 = from + G::kSliceBytes + kk * (kD * 2);
 #pragma unroll
-                    for (int mt = 0; mt < kD / 16; ++mt) {
-                        uint32_t a[4];
-                        ldsm_x4_trans(a, a0 + (((2 * mt + ((lane >> 3) & 1)) ^ (kk & 7)) << 4));
+                    for (int b = 0; b < kKS; ++b)
 #pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb) mma_16816<kF16>(o[nb][mt], a, pf[nb][0], pf[nb][1]);
-                    }
+                        for (int mt = 0; mt < kD / 16; ++mt) {
+                            uint32_t a[4];
+                            ldsm_x4_trans(a, a0 + b * (16 * kD * 2) + (((2 * mt + ((lane >> 3) & 1)) ^ (kk & 7)) << 4));
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb)
+                                mma_16816<kF16>(o[nb][mt], a, pf[nb][b][0], pf[nb][b][1]);
+                        }
                 }
             }
-            __syncwarp();  // every lane has read the stage and its mask
-            issue(st);
             st = st + 1 == G::kStages ? 0 : st + 1;
         }
 
@@ -285,9 +437,6 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
             }
         const bool whole = cur.whole();
         const int slot = 2 * static_cast<int>(blockIdx.x) + (cur.tile == 0 ? 1 : 0);
-        if (!whole && cur.tile == 0 && tid == 0)
-            sp.ws.header[blockIdx.x] = PieceHeader{sh.pieces(cur.at, cur.tiles, static_cast<int>(blockIdx.x)), cur.s,
-                                                   cur.head_unit, cur.row_unit};
         constexpr int kParts = kD / G::kMergeCols;
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
@@ -338,7 +487,15 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
                     }
                 }
             }
-        __syncthreads();  // the stats may be overwritten
+        __syncthreads();  // the stats may be overwritten; a piece is written
+        if (!whole) {
+            const int first = cur.tile == 0 ? static_cast<int>(blockIdx.x) : sh.starter(cur.at);
+            const int n = sh.pieces(cur.at, cur.tiles, first);
+            if (tid == 0) s_last = count_piece(sp.ws.count(first), n);
+            __syncthreads();
+            if (s_last) join_pieces<kF16, kD, G::kRows, G::kThreads>(p, sp, x, cur.head_unit, t0, first, n, merge);
+            __syncthreads();
+        }
     }
     cp_async_wait<0>();
 }

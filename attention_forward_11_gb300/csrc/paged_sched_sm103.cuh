@@ -11,7 +11,8 @@
 // and many short sequences needs.  A stretch that ends inside a unit leaves a piece: the
 // unnormalised sums (m, l, O) of some of its key tiles in fp32, which go to the workspace
 // and are joined by paged_combine_kernel.  Cuts that would leave a piece of less than
-// kMinPiece key tiles move to the unit's edge, and shares are at least kMinShare tiles.
+// kMinPiece key tiles move to the unit's edge, and no more blocks than units take part
+// where their shares would be below kMinShare tiles.
 //
 // With d = keys - rows of a sequence, row block i (of t tokens, the last one aside) sees
 // max(0, d + (i + 1) t) keys, an arithmetic series: the length of any number of row
@@ -25,13 +26,17 @@
 namespace attn {
 namespace paged {
 
-constexpr int kUnitKeys = 128;  // a unit's own cost, in keys
+constexpr int kUnitKeys = 256;  // a unit's own cost, in keys (about 2 us of 64 KB tiles)
 
 struct RowMap {
     int heads;      // query heads of a block
     int splits;     // blocks of heads per key/value head
     int tokens;     // tokens of a unit
     int head_units; // Hkv * splits
+    FastDiv by_heads, by_splits, by_tokens;
+    // row of a block -> token; head unit -> key/value head
+    __device__ __forceinline__ int token_of(int r) const { return static_cast<int>(by_heads.quot(r)); }
+    __device__ __forceinline__ int kv_head(int head_unit) const { return static_cast<int>(by_splits.quot(head_unit)); }
 };
 
 // How `rows` rows of a block (times `tiles` blocks side by side) cover a group.
@@ -41,6 +46,9 @@ inline RowMap make_row_map(int Hkv, int group, int rows, int tiles) {
     m.heads = (group + m.splits - 1) / m.splits;
     m.tokens = rows / m.heads * tiles;
     m.head_units = Hkv * m.splits;
+    m.by_heads = make_fastdiv(m.heads);
+    m.by_splits = make_fastdiv(m.splits);
+    m.by_tokens = make_fastdiv(m.tokens);
     return m;
 }
 
@@ -52,9 +60,13 @@ struct PieceHeader {
 
 // Workspace: headers [G], (m, l) [2 G][rows], O [2 G][rows][D].  Block c's piece at the
 // front of its share (a unit begun by an earlier block) is slot 2 c, the one at its end
-// slot 2 c + 1.
+// slot 2 c + 1.  Where the last block to finish a unit's pieces joins them, the headers'
+// place holds the counts of the pieces that are there (count_piece).
 struct Workspace {
     PieceHeader* header;
+    __device__ __forceinline__ unsigned long long* count(int c) const {
+        return reinterpret_cast<unsigned long long*>(header + c);
+    }
     float2* ml;
     float* o;
 };
@@ -68,10 +80,18 @@ __host__ __device__ inline size_t ws_bytes(int G, int rows, int D) {
 struct SchedParams {
     RowMap map;
     Workspace ws;
+    unsigned long long tag;  // of this launch, 48 bits, not zero
 };
 
+// a / b for a, b >= 0; most fit 32 bits, where a division is several times cheaper
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0)
+        return static_cast<long long>(static_cast<unsigned int>(a) / static_cast<unsigned int>(b));
+    return a / b;
+}
+
 __device__ __forceinline__ int row_units(const SchedParams& sp, const Seq& x) {
-    return (x.q_len + sp.map.tokens - 1) / sp.map.tokens;
+    return static_cast<int>(sp.map.by_tokens.quot((long long)x.q_len + sp.map.tokens - 1));
 }
 
 // Keys that row unit i sees: those of its last token.
@@ -88,7 +108,7 @@ __device__ __forceinline__ long long units_length(const PagedParams& p, const Sc
         const long long t = sp.map.tokens, d = (long long)x.kv_len - x.q_len;
         const bool all = r == row_units(sp, x);
         const long long n = all ? r - 1 : r;                // units of t tokens
-        const long long i0 = d >= 0 ? 0 : min(-d / t, n);   // the first that sees a key: d + (i0 + 1) t > 0
+        const long long i0 = d >= 0 ? 0 : min((long long)sp.map.by_tokens.quot(-d), n);   // the first that sees a key: d + (i0 + 1) t > 0
         keys = (n - i0) * d + t * ((n * (n + 1) - i0 * (i0 + 1)) / 2) + (all ? x.kv_len : 0);
     }
     return keys + (long long)r * kUnitKeys;
@@ -101,6 +121,7 @@ __device__ __forceinline__ long long seq_length(const PagedParams& p, const Sche
 // A block's share, and a position in it.  kTile: keys of a tile (a power of two).
 template <int kTile, int kMinPiece, int kMinShare>
 struct Share {
+    static_assert(kTile <= kUnitKeys, "two cuts, at least kUnitKeys apart, never fall on one tile");
     long long begin, end;  // stretch of this block
     long long total;
     int blocks;            // that have a share
@@ -116,15 +137,21 @@ struct Share {
     __device__ __forceinline__ int pieces(long long start, int tiles, int first) const {
         // cut(x) < tiles  <=>  x < kUnitKeys + kTile * (tiles - kMinPiece + 1)
         const long long y = start + kUnitKeys + (long long)kTile * (tiles - kMinPiece + 1);
-        const long long last = (y * blocks + total - 1) / total - 1;  // largest c with floor(c T / G) < y
+        const long long last = quotient(y * blocks + total - 1, total) - 1;  // largest c with floor(c T / G) < y
         return static_cast<int>(min(last, (long long)blocks - 1)) - first + 1;
+    }
+    // The block that has the first piece of a cut unit: the first whose end is no cut at
+    // the unit's start.
+    __device__ __forceinline__ int starter(long long start) const {
+        const long long y = start + kUnitKeys + (long long)kTile * kMinPiece;
+        return static_cast<int>(quotient(y * blocks + total - 1, total)) - 1;  // first c with floor((c + 1) T / G) >= y
     }
 };
 
 struct StartPos {
-    long long total;
     long long seq_at;  // position of the sequence that the share starts in
     int seq;
+    Seq x;
 };
 
 // Sum over the block (every thread calls it; kThreads / 32 <= 32 warps).
@@ -141,25 +168,30 @@ __device__ __forceinline__ long long block_sum(long long v, long long* part) {
     return v;
 }
 
-// The share of block blockIdx.x and the sequence it starts in (block-wide; `part` and
-// `found` are shared scratch).  Returns false for a block without work.
+// The share of block blockIdx.x and the sequence it starts in (block-wide; `part`, two
+// values a warp, and `found` are shared scratch).  Returns false for a block without work.
 template <int kThreads, class ShareT, int kTile, int kMinShare>
 __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedParams& sp, long long* part, StartPos* found,
                                            ShareT& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long sum = 0;
-    for (int s = tid; s < p.n_seqs; s += kThreads) sum += seq_length(p, sp, seq_of(p, s));
-    sh.total = block_sum<kThreads>(sum, part);
-    if (sh.total == 0) return false;
-    sh.blocks = static_cast<int>(min((long long)gridDim.x, max(sh.total / (kTile * kMinShare), 1ll)));
-    const int c = blockIdx.x;
-    if (c >= sh.blocks) return false;
-    sh.begin = c * sh.total / sh.blocks;
-    sh.end = (c + 1) * sh.total / sh.blocks;
+    const bool one_step = p.n_seqs <= kThreads;
+    long long n_units = 0;
+    if (!one_step) {
+        long long sum = 0;
+        for (int s = tid; s < p.n_seqs; s += kThreads) {
+            const Seq x = seq_of(p, s);
+            sum += seq_length(p, sp, x);
+            n_units += row_units(sp, x);
+        }
+        sh.total = block_sum<kThreads>(sum, part);
+        n_units = block_sum<kThreads>(n_units, part);
+    }
     long long at = 0;  // before the step's sequences
     for (int s0 = 0; s0 < p.n_seqs; s0 += kThreads) {
         const int s = s0 + tid;
-        const long long len = s < p.n_seqs ? seq_length(p, sp, seq_of(p, s)) : 0;
+        Seq x{};
+        if (s < p.n_seqs) x = seq_of(p, s);
+        const long long len = seq_length(p, sp, x);
         long long v = len;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -167,17 +199,36 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
             if (lane >= d) v += u;
         }
         if (lane == 31) part[warp] = v;
+        if (s0 == 0 && one_step) {
+            const int units = __reduce_add_sync(0xffffffffu, row_units(sp, x));
+            if (lane == 0) part[kThreads / 32 + warp] = units;
+        }
         __syncthreads();
         long long before = at, step = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += part[w];
             step += part[w];
+            if (s0 == 0 && one_step) n_units += part[kThreads / 32 + w];
+        }
+        if (s0 == 0) {
+            if (one_step) sh.total = step;
+            if (sh.total == 0) return false;
+            // a block for every unit, and more where that leaves shares of kMinShare tiles (but
+            // not a few more, which would cut every unit for little)
+            n_units *= sp.map.head_units;
+            const long long most = sh.total / (kTile * kMinShare);
+            sh.blocks = static_cast<int>(min((long long)gridDim.x, 2 * most >= 3 * n_units ? most : n_units));
+            const long long c = blockIdx.x;
+            if (c >= sh.blocks) return false;
+            sh.begin = quotient(c * sh.total, sh.blocks);
+            sh.end = quotient((c + 1) * sh.total, sh.blocks);
         }
         const long long end = before + v, start = end - len;
         if (sh.begin >= start && sh.begin < end) {
             found->seq = s;
             found->seq_at = start;
+            found->x = x;
         }
         at += step;
         __syncthreads();
@@ -242,11 +293,11 @@ struct Cursor {
     }
     __device__ __forceinline__ void first(const PagedParams& p, const SchedParams& sp, const ShareT& sh, const StartPos& f) {
         s = f.seq;
-        x = seq_of(p, s);
+        x = f.x;
         ok = true;
         n_row_units = row_units(sp, x);
         const long long per_head = units_length(p, sp, x, n_row_units);
-        head_unit = static_cast<int>((sh.begin - f.seq_at) / per_head);
+        head_unit = static_cast<int>(quotient(sh.begin - f.seq_at, per_head));
         const long long head_at = f.seq_at + head_unit * per_head, rest = sh.begin - head_at;
         int lo = 0, hi = n_row_units - 1;  // the last row unit that starts at or before the position
         while (lo < hi) {
@@ -270,16 +321,45 @@ struct Row {
 __device__ __forceinline__ Row row_of(const PagedParams& p, const RowMap& m, const Seq& x, int head_unit, int t0, int tokens,
                                       int r) {
     Row w;
-    const int t = r / m.heads, h = (head_unit % m.splits) * m.heads + r % m.heads;
+    const int t = m.token_of(r), g = m.kv_head(head_unit);
+    const int h = (head_unit - g * m.splits) * m.heads + r - t * m.heads;
     w.token = t0 + t;
-    w.head = head_unit / m.splits * p.group + h;
+    w.head = g * p.group + h;
     w.there = t < tokens && w.token < x.q_len && h < p.group;
     return w;
 }
 
-// ---- programmatic launch: the joining kernel is in place when the last block ends
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// ---- the last block to finish a unit's pieces joins them
+// Slot of piece i of a unit that block `first` starts.
+__device__ __forceinline__ int piece_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
+
+// The pieces of the unit that block c starts are counted in word c of a workspace of unknown
+// contents: the count is a launch's own once the upper 48 bits of the word are the launch's
+// tag.  Every block that will count a piece makes sure of that long before (begin_count: a
+// word that is not the launch's yet becomes its zero, by whoever comes first), so that the
+// counting itself is one atomic addition, however many blocks end together.  The block that
+// counts the last piece joins all, and clears the word: a replayed graph's launches share
+// their tag.
+struct CountWord {
+    unsigned long long* word;
+    unsigned long long seen;
+};
+__device__ __forceinline__ CountWord look_at_count(unsigned long long* word) {
+    CountWord c{word, 0};
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(c.seen) : "l"(word) : "memory");
+    return c;
+}
+__device__ __forceinline__ void begin_count(const CountWord& c, unsigned long long tag) {
+    if ((c.seen >> 16) != tag) atomicCAS(c.word, c.seen, tag << 16);
+}
+// One thread, behind a barrier that follows the piece's writes; true for the last of n.
+__device__ __forceinline__ bool count_piece(unsigned long long* word, int n) {
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+    const bool last = static_cast<int>(old & 0xffff) + 1 == n;
+    if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
+    return last;
+}
 
 // Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L.
 // Grid (G, row groups): block (c, y) has kRowsPer rows of the unit that block c of the

@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kTableThreads) paged_tables_kernel(const Table
     __shared__ long long s_tok[kTableThreads], s_page[kTableThreads];  // tokens / new pages before the sequence
     __shared__ int s_ctx[kTableThreads], s_have[kTableThreads];
     __shared__ long long s_part[2][32];
+    launch_dependents();
+    wait_for_primary();
     const int tid = threadIdx.x, G = gridDim.x, c = blockIdx.x;
     const long long head = p.free_head != nullptr ? max(*p.free_head, 0) : 0;
     // this block's share of the slot map
@@ -160,6 +162,8 @@ struct AppendParams {
 };
 
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
+    launch_dependents();
+    wait_for_primary();
     const long long row0 = (long long)blockIdx.x * p.per_block;
     const unsigned int n = static_cast<unsigned int>(min((long long)p.per_block, p.T - row0)) * p.row_chunks;
     for (unsigned int i = threadIdx.x; i < n; i += kAppendThreads) {

@@ -69,7 +69,7 @@ struct TilesGeo {
     static constexpr int kSmemMask = kSmemMmaExit + 4;
     static constexpr int kSmemStart = (kSmemMask + kMaskRing * 4 + 7) / 8 * 8;
     static constexpr int kSmemPart = kSmemStart + static_cast<int>(sizeof(StartPos));
-    static constexpr int kSmemItems = kSmemPart + kThreads / 32 * 8;
+    static constexpr int kSmemItems = kSmemPart + 2 * (kThreads / 32) * 8;
     static constexpr int kSmemUsed = kSmemItems + kItems * static_cast<int>(sizeof(Item));
     static constexpr int kSmemBytes = kSmemUsed + 1024;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     StartPos* start = reinterpret_cast<StartPos*>(smem + T::kSmemStart);
     auto bar = [&](int i) -> uint32_t { return sbase + T::kSmemBar + 8 * i; };
     launch_dependents();
+    wait_for_primary();
 
     // ---- this block's share
     typename T::ShareT sh;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // Q of a unit; a tile without key tiles needs none
         auto post_q = [&]() -> bool {
-            const int h0 = wk.head_unit / sp.map.splits * p.group + wk.head_unit % sp.map.splits * sp.map.heads;
+            const int h0 = sp.map.kv_head(wk.head_unit) * p.group + wk.head_unit % sp.map.splits * sp.map.heads;
             for (int t = 0; t < kTiles; ++t) {
                 const bool got =
                     q_issued[t] == 0 || wait_bounded(bar(BAR_QEMPTY + t), (q_issued[t] - 1) & 1, abort_flag, limit);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool valid = in_range && page >= 0 && page < p.n_pages;
             const int k_page = valid ? page : p.n_pages, k_row = valid ? page_row : 0;  // past the last page: zeros
-            const int k_hkv = wk.head_unit / sp.map.splits;
+            const int k_hkv = sp.map.kv_head(wk.head_unit);
             const uint32_t miss = __ballot_sync(0xffffffffu, in_range && !valid);
             if (lane == 0) {
                 if (have_k) {
