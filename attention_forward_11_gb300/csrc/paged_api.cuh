@@ -186,8 +186,8 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
     const attn_status_t st = launch_behind(paged_tiles_kernel<kF16, kD>, dim3(sms), attn::kThreads, T::kSmemBytes, stream,
                                            tm[0], tm[1], tm[2], p, sp, tp);
     if (st != ATTN_OK) return st;
-    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles, 8>, dim3(sms, T::kRows / 8),
-                         kCombineThreads, 0, stream, p, sp);
+    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>,
+                         dim3(sms, T::kRows / (kCombineThreads / (kD / 4))), kCombineThreads, 0, stream, p, sp);
 }
 
 template <bool kF16, int kD>

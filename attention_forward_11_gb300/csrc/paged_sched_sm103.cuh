@@ -361,91 +361,78 @@ __device__ __forceinline__ bool count_piece(unsigned long long* word, int n) {
     return last;
 }
 
-// Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L.
-// Grid (G, row groups): block (c, y) has kRowsPer rows of the unit that block c of the
-// first kernel starts; its warps share a row's pieces, in a fixed order, and add up in
-// shared memory in the order of the warps.
+// Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, the
+// sums in the order of the pieces.  Grid (G, kRows / rows of a block): block (c, y) has rows
+// of the unit that block c of the first kernel starts, kD / 4 threads a row with four columns
+// each.  Most units have two or three pieces, so what the kernel costs is its instructions a
+// row and how soon its loads start: those of the first kFly pieces do not wait for M.
 constexpr int kCombineThreads = 256;
 
-template <bool kF16, int kD, int kRows, int kTokenTiles, int kRowsPer>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedParams p, const SchedParams sp) {
-    constexpr int kWarpsPer = kCombineThreads / 32 / kRowsPer;  // warps of a row
-    constexpr int kPer = kD / 32;                               // columns of a lane
-    __shared__ float s_o[kWarpsPer > 1 ? kCombineThreads / 32 : 1][kD];
-    __shared__ float2 s_ml[kCombineThreads / 32];
+template <bool kF16, int kD, int kRows, int kTokenTiles>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __grid_constant__ PagedParams p,
+                                                                        const __grid_constant__ SchedParams sp) {
+    constexpr int kLanes = kD / 4, kFly = 4;
+    constexpr int kTileRows = kRows / kTokenTiles;
+    launch_dependents();
+    touch_params(sp);
     wait_for_primary();  // every thread: this kernel's end stands for the first one's too
     const int c = blockIdx.x;
     const PieceHeader h = sp.ws.header[c];
     if (h.n == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = warp / kWarpsPer, part = warp % kWarpsPer;
-    const int r = blockIdx.y * kRowsPer + rr;  // row of the unit
+    const int col = threadIdx.x % kLanes * 4;
+    const int r = blockIdx.y * (kCombineThreads / kLanes) + threadIdx.x / kLanes;  // row of the unit
+    const size_t tail = (size_t)(2 * c + 1) * kRows + r, head = (size_t)(2 * c) * kRows + r;  // of pieces 0 and i > 0
+    auto row_of_piece = [&](int i) { return i == 0 ? tail : head + (size_t)(2 * i) * kRows; };
+    float2 ml[kFly];
+    float4 v[kFly];
+#pragma unroll
+    for (int j = 0; j < kFly; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     const Seq x = seq_of(p, h.seq);
-    constexpr int kTileRows = kRows / kTokenTiles;
-    const int tile_tokens = sp.map.tokens / kTokenTiles;
-    const int tile = r / kTileRows;
+    const int tile_tokens = sp.map.tokens / kTokenTiles, tile = r / kTileRows;
     const Row w = row_of(p, sp.map, x, h.head_unit, h.row_unit * sp.map.tokens + tile * tile_tokens, tile_tokens,
                          r % kTileRows);
-    float M = -INFINITY, L = 0.f, acc[kPer] = {};
-    if (w.there) {
-        for (int i = lane; i < h.n; i += 32) {
-            const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-            M = fmaxf(M, sp.ws.ml[(size_t)slot * kRows + r].x);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float use = M == -INFINITY ? 0.f : M;
-        constexpr int kFly = kD == 256 ? 4 : 8;  // pieces in flight
-        for (int i0 = part; i0 < h.n; i0 += kFly * kWarpsPer) {
-            float f[kFly], v[kFly][kPer];
-#pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                const int i = i0 + j * kWarpsPer;
-                const int slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
-                f[j] = 0.f;
-                if (i < h.n) {
-                    const float2 ml = sp.ws.ml[(size_t)slot * kRows + r];
-                    f[j] = ex2_approx(ml.x - use);
-                    L += ml.y * f[j];
-                    const float* src = sp.ws.o + ((size_t)slot * kRows + r) * kD + kPer * lane;
-#pragma unroll
-                    for (int e = 0; e < kPer; e += 2) {
-                        const float2 y = *reinterpret_cast<const float2*>(src + e);
-                        v[j][e] = y.x;
-                        v[j][e + 1] = y.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) v[j][e] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kFly; ++j)
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] += v[j][e] * f[j];
-        }
-    }
-    if constexpr (kWarpsPer > 1) {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = acc[e];
-        if (lane == 0) s_ml[warp].y = L;
-        __syncthreads();
-        if (part != 0) return;
-#pragma unroll
-        for (int k = 1; k < kWarpsPer; ++k) {
-            L += s_ml[warp + k].y;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += s_o[warp + k][kPer * lane + e];
-        }
-    }
     if (!w.there) return;
+#pragma unroll
+    for (int j = 0; j < kFly; ++j)
+        if (j < h.n) {
+            ml[j] = sp.ws.ml[row_of_piece(j)];
+            v[j] = *reinterpret_cast<const float4*>(sp.ws.o + row_of_piece(j) * kD + col);
+        }
+    float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    for (int i = kFly; i < h.n; ++i) M = fmaxf(M, sp.ws.ml[row_of_piece(i)].x);
+    const float use = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0;;) {
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            const float f = ex2_approx(ml[j].x - use);
+            L += ml[j].y * f;
+            acc.x += v[j].x * f;
+            acc.y += v[j].y * f;
+            acc.z += v[j].z * f;
+            acc.w += v[j].w * f;
+        }
+        i0 += kFly;
+        if (i0 >= h.n) break;
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + j < h.n) {
+                ml[j] = sp.ws.ml[row_of_piece(i0 + j)];
+                v[j] = *reinterpret_cast<const float4*>(sp.ws.o + row_of_piece(i0 + j) * kD + col);
+            }
+        }
+    }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t tok = (size_t)x.q0 + w.token;
-    uint16_t* dst = p.o + (tok * p.Hq + w.head) * kD + kPer * lane;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack_x2<kF16>(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
+    *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
+        make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
+    if (col == 0 && p.lse != nullptr)
         p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 

@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     StartPos* start = reinterpret_cast<StartPos*>(smem + T::kSmemStart);
     auto bar = [&](int i) -> uint32_t { return sbase + T::kSmemBar + 8 * i; };
     launch_dependents();
+    touch_params(p);
+    touch_params(sp);
     wait_for_primary();
 
     // ---- this block's share
@@ -691,12 +693,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(bar(BAR_OFREE + t));
                     }
-                    if (w.slot >= 0) {  // a piece: raw sums to its workspace slot
-                        if (there) {
-                            uint4* dst = reinterpret_cast<uint4*>(sp.ws.o + ws_row * kD + 64 * h);
+                    if (w.slot >= 0) {  // a piece: raw sums to its workspace slot, 32 columns at a time
+                        float* dst = sp.ws.o + (ws_row - lane) * kD + 64 * h;  // of the warp's first row
 #pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                                    make_uint4(o[32 * c + 4 * q], o[32 * c + 4 * q + 1], o[32 * c + 4 * q + 2],
+                                               o[32 * c + 4 * q + 3]);
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int rr = 4 * i + lane / 8, q = lane % 8;
+                                *reinterpret_cast<uint4*>(dst + rr * kD + 32 * c + 4 * q) =
+                                    *reinterpret_cast<const uint4*>(stage + rr * 128 + ((q ^ (rr & 7)) * 16));
+                            }
+                            __syncwarp();
                         }
                         continue;
                     }
