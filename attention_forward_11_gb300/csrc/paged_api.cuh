@@ -174,14 +174,31 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
     if (fn(&tm[0], type, 3, const_cast<uint16_t*>(p.q), q_dims, q_strides, q_box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
            CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return ATTN_ERR_CUDA;
-    const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)p.Hkv, (cuuint64_t)p.page_size, (cuuint64_t)p.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)p.head_stride * 2, (cuuint64_t)p.token_stride * 2,
-                                   (cuuint64_t)p.page_stride * 2};
+    // K and V: boxes of box_rows rows.  A row of head size 128 is two 128-byte halves of a
+    // swizzled tile, which a tensor map of (64 columns, row, head, page) copies apart.  With
+    // the axes (64 columns, 8 rows, half, 8-row group, page) one box has both, and a head is
+    // a step of the half axis where heads follow one another in a row, or of the group axis
+    // where a head's rows of a page do.
+    const bool by_half = p.head_stride == kD, by_group = p.head_stride == p.token_stride * p.page_size;
+    const bool folded = kD == 128 && (by_half || by_group);
+    tp.halves = folded ? 1 : kD / 64;
+    tp.half_bytes = folded ? 1024 : attn::kHalfBytes;
+    tp.group_bytes = folded ? 2048 : 1024;
+    tp.head_at_half = by_half ? 2 : 0;
+    tp.head_at_group = by_half ? 0 : p.page_size / 8;
+    const cuuint64_t heads = (cuuint64_t)p.Hkv, groups = (cuuint64_t)p.page_size / 8;
+    const cuuint64_t hs = (cuuint64_t)p.head_stride * 2, ts = (cuuint64_t)p.token_stride * 2, ps = (cuuint64_t)p.page_stride * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)kD, heads, (cuuint64_t)p.page_size, (cuuint64_t)p.n_pages};
+    const cuuint64_t strides[3] = {hs, ts, ps};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)tp.box_rows, 1};
+    const cuuint64_t fold_dims[5] = {64, 8, by_half ? 2 * heads : 2, by_half ? groups : groups * heads, (cuuint64_t)p.n_pages};
+    const cuuint64_t fold_strides[4] = {ts, 128, 8 * ts, ps};
+    const cuuint32_t fold_box[5] = {64, 8, 2, (cuuint32_t)tp.box_rows / 8, 1};
+    const cuuint32_t estr5[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < 2; ++i)
-        if (fn(&tm[1 + i], type, 4, const_cast<uint16_t*>(i ? p.v : p.k), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (fn(&tm[1 + i], type, folded ? 5 : 4, const_cast<uint16_t*>(i ? p.v : p.k), folded ? fold_dims : dims,
+               folded ? fold_strides : strides, folded ? fold_box : box, estr5, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return ATTN_ERR_CUDA;
     const attn_status_t st = launch_behind(paged_tiles_kernel<kF16, kD>, dim3(sms), attn::kThreads, T::kSmemBytes, stream,
                                            tm[0], tm[1], tm[2], p, sp, tp);
@@ -190,11 +207,10 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
                          dim3(sms, T::kRows / (kCombineThreads / (kD / 4))), kCombineThreads, 0, stream, p, sp);
 }
 
+// The rows kernel's variant for sequences of at most `rows` rows.
 template <bool kF16, int kD>
-attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
-    const long long rows = (long long)max_q_len * p.group;
-    if constexpr (kD != 256)
-        if (takes_tiles(rows, kD, p.page_size)) return launch_tiles<kF16, kD>(p, workspace, sms, stream);
+attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows, void* workspace, int sms,
+                              cudaStream_t stream) {
     const int nb = row_blocks_for(rows, kD);
     if (nb == 1) return launch_rows<kF16, kD, 1>(p, workspace, sms, stream);
     if constexpr (kD != 256) {
@@ -202,6 +218,33 @@ attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, voi
         if (nb == 4) return launch_rows<kF16, kD, 4>(p, workspace, sms, stream);
     }
     return launch_rows<kF16, kD, 2>(p, workspace, sms, stream);
+}
+
+// Are there likely to be single tokens among the long sequences?  The lengths are on the
+// device; on the host the longest one against the mean tells.  A row tile of 128 with one
+// token in it costs 1.7 us a key tile however few rows it has, where the rows kernel
+// streams the cache, but the rows kernel costs 2.5 us when there is nothing for it.
+bool is_mixed(const attn::paged::PagedParams& p, int max_q_len) {
+    return p.group <= 32 && (long long)max_q_len * p.n_seqs >= 4ll * p.total_q && p.n_seqs > 1;
+}
+
+template <bool kF16, int kD>
+attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
+    const long long rows = (long long)max_q_len * p.group;
+    if constexpr (kD != 256) {
+        if (takes_tiles(rows, kD, p.page_size)) {
+            attn::paged::PagedParams half = p;
+            if (is_mixed(p, max_q_len)) {
+                half.split_rows = 8 * row_blocks_for(p.group, kD);
+                half.take_short = 1;
+                const attn_status_t st = launch_rows_for<kF16, kD>(half, p.group, workspace, sms, stream);
+                if (st != ATTN_OK) return st;
+                half.take_short = 0;
+            }
+            return launch_tiles<kF16, kD>(half, workspace, sms, stream);
+        }
+    }
+    return launch_rows_for<kF16, kD>(p, rows, workspace, sms, stream);
 }
 
 }  // namespace

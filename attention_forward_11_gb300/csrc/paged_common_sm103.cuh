@@ -40,6 +40,9 @@ struct PagedParams {
     long long page_stride, token_stride, head_stride;  // of both caches, in elements
     float scale_log2;                                 // softmax scale * log2(e)
     FastDiv by_page;
+    // A batch shared by two kernels: sequences of at most split_rows (token, head) rows a
+    // key/value head are the first one's (take_short), the others the second one's.  0: all.
+    int split_rows, take_short;
 };
 
 struct Seq {
@@ -51,6 +54,7 @@ __device__ __forceinline__ Seq seq_of(const PagedParams& p, int s) {
     x.q0 = min(max(p.cu_q[s], 0), p.total_q);
     x.q_len = max(min(p.cu_q[s + 1], p.total_q) - x.q0, 0);
     x.kv_len = min(max(p.kv_lens[s], 0), p.max_kv);
+    if (p.split_rows != 0 && (x.q_len * p.group <= p.split_rows) != (p.take_short != 0)) x.q_len = 0;
     return x;
 }
 

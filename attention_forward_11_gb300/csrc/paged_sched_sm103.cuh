@@ -299,11 +299,16 @@ struct Cursor {
         const long long per_head = units_length(p, sp, x, n_row_units);
         head_unit = static_cast<int>(quotient(sh.begin - f.seq_at, per_head));
         const long long head_at = f.seq_at + head_unit * per_head, rest = sh.begin - head_at;
-        int lo = 0, hi = n_row_units - 1;  // the last row unit that starts at or before the position
-        while (lo < hi) {
-            const int mid = lo + (hi - lo + 1) / 2;
-            if (units_length(p, sp, x, mid) <= rest) lo = mid;
-            else hi = mid - 1;
+        // the last row unit that starts at or before the position: the warp's lanes try 32 at
+        // a time (every lane of a warp calls this)
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = n_row_units;  // it is one of [lo, lo + n)
+        while (n > 1) {
+            const int step = (n + 31) / 32, at_lane = lo + lane * step;
+            const bool before = lane * step < n && units_length(p, sp, x, at_lane) <= rest;  // lane 0: true
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
+            n = min(step, n - k * step);
+            lo += k * step;
         }
         row_unit = lo;
         at = head_at + units_length(p, sp, x, lo);

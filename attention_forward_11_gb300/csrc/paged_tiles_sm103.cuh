@@ -35,7 +35,7 @@ namespace paged {
 
 constexpr int kSchedWarp = kMmaWarp + 3;
 constexpr int kItems = 4;       // work items posted ahead
-constexpr int kMaskRing = 8;    // page masks of the last K tiles: three are in use at most
+constexpr int kMaskRing = 8;    // page masks of the last K tiles
 constexpr int kItemReaders = kSoftmaxWarps + 4 + 2;  // warps that read an item
 
 struct Item {
@@ -48,22 +48,42 @@ struct Item {
     __device__ __forceinline__ int nmax() const { return n0 > n1 ? n0 : n1; }
 };
 
-enum : int {
-    BAR_ITEMFULL = BAR_COUNT,
-    BAR_ITEMEMPTY = BAR_ITEMFULL + kItems,
-    BAR_PAGED_COUNT = BAR_ITEMEMPTY + kItems
-};
-
 template <int kD>
 struct TilesGeo {
-    using G = Geo<kD>;
+    static_assert(kD == 64 || kD == 128, "head size 64 or 128");
     static constexpr int kTile = kBN;
     static constexpr int kRows = kTiles * kBM;
     static constexpr int kMinPiece = 2, kMinShare = 4;
     using ShareT = Share<kTile, kMinPiece, kMinShare>;
     using CursorT = Cursor<ShareT, kTile>;
-    static constexpr int kSmemBar = G::kSmemBar;
-    static constexpr int kSmemTmemSlot = kSmemBar + BAR_PAGED_COUNT * 8;
+    // K/V stages in flight: what fits beside Q.  Two of 64 KB at head size 128; four of 32 KB
+    // at 64, where the boxes of a tile take as long to issue (1700 cycles for 16) but the
+    // products half as long: with two the tensor cores wait for them.
+    static constexpr int kStages = kD == 64 ? 4 : 2;
+    static constexpr int kHalves = kD / 64;
+    static constexpr int kTileBytes = kBM * kD * 2;  // Q, K or V tile
+    // barriers, as in the dense forward, and those of the work items
+    static constexpr int kBarQFull = 0;
+    static constexpr int kBarQEmpty = kBarQFull + kTiles;
+    static constexpr int kBarKvFull = kBarQEmpty + kTiles;     // [stage]: V_{g-1} and K_g landed
+    static constexpr int kBarKvEmpty = kBarKvFull + kStages;   // [stage]: both read by their last MMA
+    static constexpr int kBarSFull = kBarKvEmpty + kStages;
+    static constexpr int kBarODone = kBarSFull + kTiles;
+    static constexpr int kBarOFree = kBarODone + kTiles;
+    static constexpr int kBarStatsFull = kBarOFree + kTiles;
+    static constexpr int kBarStatsFree = kBarStatsFull + kTiles;
+    static constexpr int kBarMmaDone = kBarStatsFree + kTiles;
+    static constexpr int kBarItemFull = kBarMmaDone + 1;
+    static constexpr int kBarItemEmpty = kBarItemFull + kItems;
+    static constexpr int kBarCount = kBarItemEmpty + kItems;
+    // shared memory, from a 1024-byte aligned base
+    static constexpr int kSmemQ = 0;
+    static constexpr int kSmemK = kSmemQ + kTiles * kTileBytes;
+    static constexpr int kSmemV = kSmemK + kStages * kTileBytes;
+    static constexpr int kSmemStage = kSmemV + kStages * kTileBytes;  // O staging: 4 KB a warp
+    static constexpr int kSmemStats = kSmemStage + kHalfBytes;        // per tile and row: (m, l)
+    static constexpr int kSmemBar = kSmemStats + kTiles * kBM * 8;
+    static constexpr int kSmemTmemSlot = kSmemBar + kBarCount * 8;
     static constexpr int kSmemAbort = kSmemTmemSlot + 4;
     static constexpr int kSmemMmaExit = kSmemAbort + 4;
     static constexpr int kSmemMask = kSmemMmaExit + 4;
@@ -73,10 +93,20 @@ struct TilesGeo {
     static constexpr int kSmemUsed = kSmemItems + kItems * static_cast<int>(sizeof(Item));
     static constexpr int kSmemBytes = kSmemUsed + 1024;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
+    static_assert(kStages + 2 < kMaskRing, "a K tile's page mask is read before it is replaced");
 };
 
 struct TilesParams {
     int box_rows;   // rows of a K/V box: gcd(page_size, 128)
+    // A K/V tile in shared memory: 8-row groups of 128-byte rows, `group_bytes` apart, and
+    // the second 64 columns (head size 128) `half_bytes` behind the first.  Copied half by
+    // half, the halves are 16 KB blocks (1024 and 16384).  Where the cache's strides let
+    // a tensor map step over a row's two halves inside a group (paged_api.cuh), one box has
+    // both, and the groups of the halves alternate (2048 and 1024): half the copies.
+    int half_bytes, group_bytes;
+    int halves;          // halves that are copied apart: 2 or 1
+    int head_at_half;    // coordinates of a folded box: third = head * head_at_half,
+    int head_at_group;   // fourth = head * head_at_group + row / 8
     int tile_tokens;  // tokens of a row tile
     int q_rows;       // rows that a Q box fills
     unsigned int poll_limit;
@@ -92,13 +122,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "l"(policy)
+        : "memory");
+}
+
 template <bool kF16, int kD>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p,
                        const __grid_constant__ SchedParams sp, const __grid_constant__ TilesParams tp) {
-    using G = Geo<kD>;
     using T = TilesGeo<kD>;
+    constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
@@ -114,35 +153,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     launch_dependents();
     touch_params(p);
     touch_params(sp);
-    wait_for_primary();
 
-    // ---- this block's share
-    typename T::ShareT sh;
-    if (threadIdx.x == 0) sp.ws.header[blockIdx.x].n = 0;
-    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare>(
-            p, sp, reinterpret_cast<long long*>(smem + T::kSmemPart), start, sh))
-        return;
-
-    // ---- set-up: barriers, abort flag, tensor memory
+    // ---- set-up: barriers, abort flag, tensor memory (the kernel in front may still run)
     if (warp == kLoadWarp && lane == 0) {
         for (int t = 0; t < kTiles; ++t) {
-            mbar_init(bar(BAR_QFULL + t), 1);
-            mbar_init(bar(BAR_QEMPTY + t), 1);
-            mbar_init(bar(BAR_SFULL + t), 1);
-            mbar_init(bar(BAR_ODONE + t), 1);
-            mbar_init(bar(BAR_OFREE + t), 4 * 32);
-            mbar_init(bar(BAR_STATSFULL + t), 4 * 32);
-            mbar_init(bar(BAR_STATSFREE + t), 4 * 32);
+            mbar_init(bar(T::kBarQFull + t), 1);
+            mbar_init(bar(T::kBarQEmpty + t), 1);
+            mbar_init(bar(T::kBarSFull + t), 1);
+            mbar_init(bar(T::kBarODone + t), 1);
+            mbar_init(bar(T::kBarOFree + t), 4 * 32);
+            mbar_init(bar(T::kBarStatsFull + t), 4 * 32);
+            mbar_init(bar(T::kBarStatsFree + t), 4 * 32);
         }
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bar(BAR_KVFULL + s), 1);
-            mbar_init(bar(BAR_KVEMPTY + s), 1);
+            mbar_init(bar(T::kBarKvFull + s), 1);
+            mbar_init(bar(T::kBarKvEmpty + s), 1);
         }
         for (int i = 0; i < kItems; ++i) {
-            mbar_init(bar(BAR_ITEMFULL + i), 1);
-            mbar_init(bar(BAR_ITEMEMPTY + i), kItemReaders);
+            mbar_init(bar(T::kBarItemFull + i), 1);
+            mbar_init(bar(T::kBarItemEmpty + i), kItemReaders);
         }
-        mbar_init(bar(BAR_MMADONE), 1);
+        mbar_init(bar(T::kBarMmaDone), 1);
         *abort_flag = 0;
         *mma_exit = 0;
         fence_mbar_init();
@@ -161,9 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned int limit = tp.poll_limit;
     const int wg = warp / 4;
 
+    // ---- this block's share
+    wait_for_primary();
+    typename T::ShareT sh;
+    if (threadIdx.x == 0) sp.ws.header[blockIdx.x].n = 0;
+    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare>(
+            p, sp, reinterpret_cast<long long*>(smem + T::kSmemPart), start, sh)) {
+        if (warp == 0) tmem_dealloc(tmem_base, kTmemCols);
+        return;
+    }
+
     // Item j, for every lane of the warp; false: no more items, or the block gives up (*ok).
     auto get_item = [&](int j, Item& w, bool& ok) -> bool {
-        const bool got = wait_bounded(bar(BAR_ITEMFULL + j % kItems), (j / kItems) & 1, abort_flag, limit);
+        const bool got = wait_bounded(bar(T::kBarItemFull + j % kItems), (j / kItems) & 1, abort_flag, limit);
         if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             return false;
@@ -180,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.n1 = it.n1;
         w.slot = it.slot;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_ITEMEMPTY + j % kItems));
+        if (lane == 0) mbar_arrive(bar(T::kBarItemEmpty + j % kItems));
         return w.n0 >= 0;
     };
 
@@ -207,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cur.next(p, sp, sh);
             }
             if (j >= kItems) {
-                const bool got = wait_bounded(bar(BAR_ITEMEMPTY + j % kItems), (j / kItems - 1) & 1, abort_flag, limit);
+                const bool got = wait_bounded(bar(T::kBarItemEmpty + j % kItems), (j / kItems - 1) & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) break;
             }
             const bool more = cur.ok;
@@ -240,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     it.n0 = -1;
                 }
-                mbar_arrive(bar(BAR_ITEMFULL + j % kItems));
+                mbar_arrive(bar(T::kBarItemFull + j % kItems));
             }
             __syncwarp();
             if (!more) break;
@@ -253,10 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile, half (lane % 16) % halves of its columns.
         const uint64_t pol_q = l2_policy_evict_first();
         const uint64_t pol_kv = l2_policy_evict_last();
-        const int box = (lane & 15) / G::kHalves, half = (lane & 15) % G::kHalves;
+        const int box = (lane & 15) / tp.halves, half = (lane & 15) % tp.halves;
+        const bool folded = tp.halves < T::kHalves;
         const int n_boxes = kBM / tp.box_rows;
         const bool copies = box < n_boxes;
-        const uint32_t box_at = half * kHalfBytes + box * tp.box_rows * 128;
+        const uint32_t box_at = half * kHalfBytes + box * (tp.box_rows / 8) * tp.group_bytes;
         int g = 0;                       // stages issued
         int q_issued[kTiles] = {0, 0};   // Q_t fills posted so far
         bool ok = true;
@@ -280,16 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h0 = sp.map.kv_head(wk.head_unit) * p.group + wk.head_unit % sp.map.splits * sp.map.heads;
             for (int t = 0; t < kTiles; ++t) {
                 const bool got =
-                    q_issued[t] == 0 || wait_bounded(bar(BAR_QEMPTY + t), (q_issued[t] - 1) & 1, abort_flag, limit);
+                    q_issued[t] == 0 || wait_bounded(bar(T::kBarQEmpty + t), (q_issued[t] - 1) & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) return false;
                 if (lane == 0) {
                     if (wk.n(t) > 0) {
-                        mbar_arrive_expect_tx(bar(BAR_QFULL + t), G::kHalves * tp.q_rows * 128);
-                        for (int h = 0; h < G::kHalves; ++h)
-                            tma_load_3d(sbase + G::kSmemQ + t * G::kTileBytes + h * kHalfBytes, &tm_q, h * 64, h0,
-                                        wk.q0 + wk.t0 + t * tp.tile_tokens, bar(BAR_QFULL + t), pol_q);
+                        mbar_arrive_expect_tx(bar(T::kBarQFull + t), T::kHalves * tp.q_rows * 128);
+                        for (int h = 0; h < T::kHalves; ++h)
+                            tma_load_3d(sbase + T::kSmemQ + t * T::kTileBytes + h * kHalfBytes, &tm_q, h * 64, h0,
+                                        wk.q0 + wk.t0 + t * tp.tile_tokens, bar(T::kBarQFull + t), pol_q);
                     } else {
-                        mbar_arrive(bar(BAR_QFULL + t));
+                        mbar_arrive(bar(T::kBarQFull + t));
                     }
                 }
                 ++q_issued[t];
@@ -301,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (have_k) look_up();
         while (ok && (have_k || have_v)) {
             const int st = g % kStages, use = g / kStages;
-            const bool got = use == 0 || wait_bounded(bar(BAR_KVEMPTY + st), (use - 1) & 1, abort_flag, limit);
+            const bool got = use == 0 || wait_bounded(bar(T::kBarKvEmpty + st), (use - 1) & 1, abort_flag, limit);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
@@ -315,18 +357,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t mask = 0;  // one bit per 16 keys
                     const int per = tp.box_rows / 16;
                     for (int b = 0; miss != 0 && b < n_boxes; ++b)
-                        if ((miss >> (b * G::kHalves)) & 1) mask |= ((1u << per) - 1u) << (b * per);
+                        if ((miss >> (b * tp.halves)) & 1) mask |= ((1u << per) - 1u) << (b * per);
                     page_mask[g % kMaskRing] = mask;
                 }
-                mbar_arrive_expect_tx(bar(BAR_KVFULL + st), ((have_k ? 1 : 0) + (have_v ? 1 : 0)) * G::kTileBytes);
+                mbar_arrive_expect_tx(bar(T::kBarKvFull + st), ((have_k ? 1 : 0) + (have_v ? 1 : 0)) * T::kTileBytes);
             }
             __syncwarp();
-            if (copies && lane < 16 && have_k)
-                tma_load_4d(sbase + G::kSmemK + st * G::kTileBytes + box_at, &tm_k, half * 64, k_hkv, k_row, k_page,
-                            bar(BAR_KVFULL + st), pol_kv);
-            if (copies && lane >= 16 && have_v)
-                tma_load_4d(sbase + G::kSmemV + ((g - 1) % kStages) * G::kTileBytes + box_at, &tm_v, half * 64, v_hkv,
-                            v_row, v_page, bar(BAR_KVFULL + st), pol_kv);
+            if (copies && (lane < 16 ? have_k : have_v)) {
+                const bool is_k = lane < 16;
+                const uint32_t to = sbase + box_at + (is_k ? T::kSmemK + st * T::kTileBytes
+                                                           : T::kSmemV + ((g - 1) % kStages) * T::kTileBytes);
+                const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+                const int hkv = is_k ? k_hkv : v_hkv, row = is_k ? k_row : v_row, pg = is_k ? k_page : v_page;
+                if (folded)
+                    tma_load_5d(to, map, 0, 0, hkv * tp.head_at_half, hkv * tp.head_at_group + row / 8, pg,
+                                bar(T::kBarKvFull + st), pol_kv);
+                else
+                    tma_load_4d(to, map, half * 64, hkv, row, pg, bar(T::kBarKvFull + st), pol_kv);
+            }
             __syncwarp();
             ++g;  // counted before anything can fail: the drain below waits for these copies
             if (have_k && ktk == 0 && !post_q()) {
@@ -348,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // drain: every copy this warp issued has landed before the block may exit
         if (lane == 0) {
             for (int t = 0; t < kTiles; ++t)
-                if (q_issued[t] > 0) drain_bounded(bar(BAR_QFULL + t), (q_issued[t] - 1) & 1, limit);
+                if (q_issued[t] > 0) drain_bounded(bar(T::kBarQFull + t), (q_issued[t] - 1) & 1, limit);
             for (int st = 0; st < kStages; ++st) {
                 const int fills = g > st ? (g - 1 - st) / kStages + 1 : 0;
-                if (fills) drain_bounded(bar(BAR_KVFULL + st), (fills - 1) & 1, limit);
+                if (fills) drain_bounded(bar(T::kBarKvFull + st), (fills - 1) & 1, limit);
             }
         }
         __syncwarp();
@@ -359,63 +407,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         // =========================== MMA issuer =============================
         constexpr uint32_t idesc_qk = idesc_f16kind_f32(kBM, kBN, false, kF16);
         constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kD, true, kF16);
-        const uint64_t q_desc0 = sdesc_sw128(sbase + G::kSmemQ, 16, 1024);
-        const uint64_t k_desc0 = sdesc_sw128(sbase + G::kSmemK, 16, 1024);
-        const uint64_t v_desc0 = sdesc_sw128(sbase + G::kSmemV, kHalfBytes, 1024);
+        const uint64_t q_desc0 = sdesc_sw128(sbase + T::kSmemQ, 16, 1024);
+        const uint64_t k_desc0 = sdesc_sw128(sbase + T::kSmemK, 16, tp.group_bytes);
+        const uint64_t v_desc0 = sdesc_sw128(sbase + T::kSmemV, tp.half_bytes, tp.group_bytes);
+        const uint64_t k_half = static_cast<uint64_t>(tp.half_bytes >> 4);   // K: to its second half's columns
+        const uint64_t v_step = static_cast<uint64_t>(tp.group_bytes >> 3);  // V: 16 keys = two groups
         auto issue_qk = [&](int t, int ks) {
             const uint32_t d = tmem_base + kTmemS + 128 * t;
-            const uint64_t qd = q_desc0 + static_cast<uint64_t>((t * G::kTileBytes) >> 4);
-            const uint64_t kd = k_desc0 + static_cast<uint64_t>((ks * G::kTileBytes) >> 4);
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>((t * T::kTileBytes) >> 4);
+            const uint64_t kd = k_desc0 + static_cast<uint64_t>((ks * T::kTileBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk) {
                 const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
-                mma_bf16_ss(d, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+                mma_bf16_ss(d, qd + off, kd + (kk >> 2) * k_half + static_cast<uint64_t>((kk & 3) * 2), idesc_qk,
+                            kk > 0 ? 1u : 0u);
             }
         };
         auto issue_pv = [&](int t, int vs, int h, bool accumulate) {
             const uint32_t d = tmem_base + kTmemO + 128 * t;
             const uint32_t pa = tmem_base + kTmemS + 128 * t;
-            const uint64_t vd = v_desc0 + static_cast<uint64_t>((vs * G::kTileBytes) >> 4);
+            const uint64_t vd = v_desc0 + static_cast<uint64_t>((vs * T::kTileBytes) >> 4);
 #pragma unroll
             for (int q = 0; q < kBN / 32; ++q) {
                 const int kk = h * (kBN / 32) + q;
-                mma_bf16_ts(d, pa + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
+                mma_bf16_ts(d, pa + kk * 8, vd + kk * v_step, idesc_pv,
                             (accumulate || kk > 0) ? 1u : 0u);
             }
         };
         int kv = 0;  // K/V tiles consumed so far (stage kv carries K_kv)
         bool ok = true;
-        for (int j = 0; ok; ++j) {
-            Item w;
-            if (!get_item(j, w, ok)) break;
-            const int nm = w.nmax();
-            bool k_ready = false;
-            for (int t = 0; t < kTiles && ok; ++t) {
-                ok = wait_bounded(bar(BAR_QFULL + t), j & 1, abort_flag, limit);
-                if (!ok) break;
-                if (w.n(t) > 0 && !k_ready) {
-                    ok = wait_bounded(bar(BAR_KVFULL + kv % kStages), (kv / kStages) & 1, abort_flag, limit);
-                    if (!ok) break;
-                    k_ready = true;
+        // S_t(0) of item j from the K of stage `st`, which has landed
+        auto first_s = [&](int j, const Item& w, int t, int st) -> bool {
+            if (!wait_bounded(bar(T::kBarQFull + t), j & 1, abort_flag, limit)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                if (w.n(t) > 0) {
+                    issue_qk(t, st);
+                    mma_commit(bar(T::kBarSFull + t));
                 }
-                tc_fence_after();
-                if (elect_one()) {
-                    if (w.n(t) > 0) {
-                        issue_qk(t, kv % kStages);
-                        mma_commit(bar(BAR_SFULL + t));
-                    }
-                    if (w.n(t) <= 1) mma_commit(bar(BAR_QEMPTY + t));  // Q_t no longer read
-                }
-                __syncwarp();
+                if (w.n(t) <= 1) mma_commit(bar(T::kBarQEmpty + t));  // Q_t no longer read
             }
-            if (!ok) break;
-            // stage kv: its V was read by the previous unit's last P.V, its K now
-            if (elect_one()) mma_commit(bar(BAR_KVEMPTY + kv % kStages));
             __syncwarp();
+            return true;
+        };
+        Item w;
+        bool have = get_item(0, w, ok);
+        if (have) {
+            ok = wait_bounded(bar(T::kBarKvFull), 0, abort_flag, limit) && first_s(0, w, 0, 0) && first_s(0, w, 1, 0);
+            if (ok && elect_one()) mma_commit(bar(T::kBarKvEmpty));  // stage 0 holds K_0 alone
+            __syncwarp();
+        }
+        for (int j = 0; ok && have; ++j) {
+            const int nm = w.nmax();
+            Item wn;
+            bool have_n = false;
             for (int kt = 0; ok && kt < nm; ++kt) {
                 const int vs = kv % kStages;
-                const int kn = kv + 1;  // stage kn: V_{kt} and K_{kt+1} (or the next unit's K_0)
-                if (!wait_bounded(bar(BAR_KVFULL + kn % kStages), (kn / kStages) & 1, abort_flag, limit)) {
+                const int kn = kv + 1;  // stage kn: V_{kt} and K_{kt+1} (or the next item's K_0)
+                const bool last = kt + 1 == nm;
+                if (last) have_n = get_item(j + 1, wn, ok);
+                if (!ok || !wait_bounded(bar(T::kBarKvFull + kn % kStages), (kn / kStages) & 1, abort_flag, limit)) {
                     ok = false;
                     break;
                 }
@@ -426,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the first P.V of a unit overwrites O_t: the previous unit's
                         // epilogue must have read it out of tensor memory
                         if (kt == 0 && j > 0 &&
-                            !wait_bounded(bar(BAR_OFREE + t), (j - 1) & 1, abort_flag, limit)) {
+                            !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit)) {
                             ok = false;
                             break;
                         }
@@ -435,43 +486,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_after();
                             if (elect_one()) {
                                 issue_pv(t, vs, h, kt > 0);
-                                if (h == 1 && kt == nt - 1) mma_commit(bar(BAR_ODONE + t));  // O_t final
+                                if (h == 1 && kt == nt - 1) mma_commit(bar(T::kBarODone + t));  // O_t final
                             }
                             __syncwarp();
                         }
-                        if (!ok) break;
                     } else if (nt == 0 && kt == 0) {
                         // tile without work: its (all-zero) O_t is "final" once the previous
                         // unit's was read, which keeps the barrier in step with the epilogue
-                        if (j > 0 && !wait_bounded(bar(BAR_OFREE + t), (j - 1) & 1, abort_flag, limit)) {
+                        if (j > 0 && !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit)) {
                             ok = false;
                             break;
                         }
-                        if (elect_one()) mma_commit(bar(BAR_ODONE + t));
+                        if (elect_one()) mma_commit(bar(T::kBarODone + t));
                         __syncwarp();
                     }
                     if (kt + 1 < nt) {
                         if (elect_one()) {
                             issue_qk(t, kn % kStages);
-                            mma_commit(bar(BAR_SFULL + t));
-                            if (kt + 2 == nt) mma_commit(bar(BAR_QEMPTY + t));  // last S_t of the unit
+                            mma_commit(bar(T::kBarSFull + t));
+                            if (kt + 2 == nt) mma_commit(bar(T::kBarQEmpty + t));  // last S_t of the unit
                         }
                         __syncwarp();
+                    } else if (last && have_n) {
+                        // the next item's S_t(0), before the other tile's last P.V: its
+                        // softmax starts while this item ends
+                        if (!first_s(j + 1, wn, t, kn % kStages)) {
+                            ok = false;
+                            break;
+                        }
                     }
                 }
                 if (!ok) break;
-                // stage kn is free once V_kt and K_{kt+1} have been read; after the unit's
-                // last step its K belongs to the next unit and is released there
-                if (kt + 1 < nm && elect_one()) mma_commit(bar(BAR_KVEMPTY + kn % kStages));
+                // stage kn is free once its V and its K have been read
+                if ((!last || have_n) && elect_one()) mma_commit(bar(T::kBarKvEmpty + kn % kStages));
                 __syncwarp();
                 ++kv;
             }
+            have = have_n;
+            w = wn;
         }
         *mma_exit = 1;  // the release warp may stop
         // every MMA this warp issued has completed before tensor memory is freed
         if (elect_one()) {
-            mma_commit(bar(BAR_MMADONE));
-            drain_bounded(bar(BAR_MMADONE), 0, limit);
+            mma_commit(bar(T::kBarMmaDone));
+            drain_bounded(bar(T::kBarMmaDone), 0, limit);
         }
         __syncwarp();
       } else {
@@ -517,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l_run = 0.f;        // running sum of weights
 
             for (int kt = 0; kt < nt; ++kt, ++sc) {
-                const bool got = wait_bounded(bar(BAR_SFULL + t), sc & 1, abort_flag, limit);
+                const bool got = wait_bounded(bar(T::kBarSFull + t), sc & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
@@ -547,16 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // V's rows behind the last key become zero.  V_kt lands with stage kv + kt + 1,
                     // which is not refilled before this tile's weights have been used.
                     const int sn = kv + kt + 1;
-                    const bool landed = wait_bounded(bar(BAR_KVFULL + sn % kStages), (sn / kStages) & 1, abort_flag, limit);
+                    const bool landed = wait_bounded(bar(T::kBarKvFull + sn % kStages), (sn / kStages) & 1, abort_flag, limit);
                     if (!__all_sync(0xffffffffu, landed)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* v = smem + G::kSmemV + ((kv + kt) % kStages) * G::kTileBytes;
-                    const int first = (w.kv_len - key0) * 8;  // 16-byte pieces of a half
-                    for (int h = 0; h < G::kHalves; ++h)
+                    uint8_t* v = smem + T::kSmemV + ((kv + kt) % kStages) * T::kTileBytes;
+                    const int first = (w.kv_len - key0) * 8;  // 16-byte pieces of a half, 64 a group
+                    for (int h = 0; h < T::kHalves; ++h)
                         for (int i = first + r; i < kBN * 8; i += 128)
-                            *reinterpret_cast<uint4*>(v + h * kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(v + h * tp.half_bytes + (i >> 6) * tp.group_bytes + (i & 63) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 // tile maximum (three-input max, 8 independent chains)
@@ -636,13 +695,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             kv += w.nmax();
 
             // hand (m, l) of every row to the epilogue warpgroup and start the next unit
-            const bool got = j == 0 || wait_bounded(bar(BAR_STATSFREE + t), (j - 1) & 1, abort_flag, limit);
+            const bool got = j == 0 || wait_bounded(bar(T::kBarStatsFree + t), (j - 1) & 1, abort_flag, limit);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
             }
-            reinterpret_cast<float2*>(smem + G::kSmemStats)[t * kBM + r] = make_float2(m_run, l_run);
-            mbar_arrive(bar(BAR_STATSFULL + t));
+            reinterpret_cast<float2*>(smem + T::kSmemStats)[t * kBM + r] = make_float2(m_run, l_run);
+            mbar_arrive(bar(T::kBarStatsFull + t));
         }
     } else {
         // =========================== epilogue warpgroup =====================
@@ -650,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp % 4;
         const int r = wq * 32 + lane;  // row within a tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        uint8_t* stage = smem + G::kSmemStage + wq * 4096;  // this warp's 32 rows of 128 bytes
+        uint8_t* stage = smem + T::kSmemStage + wq * 4096;  // this warp's 32 rows of 128 bytes
         const int row_token = r / sp.map.heads, row_head = r % sp.map.heads;
         bool ok = true;
         for (int j = 0; ok; ++j) {
@@ -660,15 +719,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = w.head_unit / sp.map.splits * p.group + h_in;
             for (int t = 0; t < kTiles; ++t) {
                 // O_t final (every P.V of the unit completed) and (m, l) of its rows
-                const bool got = wait_bounded(bar(BAR_ODONE + t), j & 1, abort_flag, limit) &&
-                                 wait_bounded(bar(BAR_STATSFULL + t), j & 1, abort_flag, limit);
+                const bool got = wait_bounded(bar(T::kBarODone + t), j & 1, abort_flag, limit) &&
+                                 wait_bounded(bar(T::kBarStatsFull + t), j & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float2 ml = reinterpret_cast<const float2*>(smem + G::kSmemStats)[t * kBM + r];
-                mbar_arrive(bar(BAR_STATSFREE + t));
+                const float2 ml = reinterpret_cast<const float2*>(smem + T::kSmemStats)[t * kBM + r];
+                mbar_arrive(bar(T::kBarStatsFree + t));
                 const int nt = w.n(t);
                 const int token = w.t0 + t * tp.tile_tokens + row_token;
                 const bool there = row_token < tp.tile_tokens && token < w.q_len && h_in < p.group;
@@ -678,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv_l = ml.y == 0.f ? 0.f : 1.f / ml.y;
                 const size_t ws_row = static_cast<size_t>(w.slot >= 0 ? w.slot : 0) * T::kRows + t * kBM + r;
 #pragma unroll
-                for (int h = 0; h < G::kHalves; ++h) {
+                for (int h = 0; h < T::kHalves; ++h) {
                     uint32_t o[64];
                     if (nt > 0) {
                         tmem_ld32(tO + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
@@ -689,10 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 64; ++e) o[e] = 0u;
                     }
-                    if (h == G::kHalves - 1) {  // O_t may now be overwritten by the next item's first P.V
+                    if (h == T::kHalves - 1) {  // O_t may now be overwritten by the next item's first P.V
                         tc_fence_before();
-                        mbar_arrive(bar(BAR_OFREE + t));
+                        mbar_arrive(bar(T::kBarOFree + t));
                     }
+                    if (w.slot >= 0 && !__any_sync(0xffffffffu, there)) continue;
                     if (w.slot >= 0) {  // a piece: raw sums to its workspace slot, 32 columns at a time
                         float* dst = sp.ws.o + (ws_row - lane) * kD + 64 * h;  // of the warp's first row
 #pragma unroll
