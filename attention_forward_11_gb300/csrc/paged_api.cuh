@@ -57,9 +57,10 @@ bool opt_in_smem_rows_all() {
                 opt_in_smem_rows<kF16, kD, 3>() && opt_in_smem_rows<kF16, kD, 4>();
 }
 
-template <bool kF16, int kD>
+template <bool kF16, int kD, bool kFold = false>
 bool opt_in_smem_tiles() {
-    return cudaFuncSetAttribute(attn::paged::paged_tiles_kernel<kF16, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(attn::paged::paged_tiles_kernel<kF16, kD, kFold>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 attn::paged::TilesGeo<kD>::kSmemBytes) == cudaSuccess;
 }
 
@@ -73,7 +74,8 @@ bool paged_device_setup(int dev, int* sm_count) {
         if (!opt_in_smem_rows_all<false, 64>() || !opt_in_smem_rows_all<true, 64>() ||
             !opt_in_smem_rows_all<false, 128>() || !opt_in_smem_rows_all<true, 128>() ||
             !opt_in_smem_tiles<false, 64>() || !opt_in_smem_tiles<true, 64>() || !opt_in_smem_tiles<false, 128>() ||
-            !opt_in_smem_tiles<true, 128>() || !opt_in_smem_rows_all<false, 256>() || !opt_in_smem_rows_all<true, 256>() ||
+            !opt_in_smem_tiles<true, 128>() || !opt_in_smem_tiles<false, 128, true>() ||
+            !opt_in_smem_tiles<true, 128, true>() || !opt_in_smem_rows_all<false, 256>() || !opt_in_smem_rows_all<true, 256>() ||
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
             return false;
         sms[dev] = n;
@@ -181,9 +183,6 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
     // where a head's rows of a page do.
     const bool by_half = p.head_stride == kD, by_group = p.head_stride == p.token_stride * p.page_size;
     const bool folded = kD == 128 && (by_half || by_group);
-    tp.halves = folded ? 1 : kD / 64;
-    tp.half_bytes = folded ? 1024 : attn::kHalfBytes;
-    tp.group_bytes = folded ? 2048 : 1024;
     tp.head_at_half = by_half ? 2 : 0;
     tp.head_at_group = by_half ? 0 : p.page_size / 8;
     const cuuint64_t heads = (cuuint64_t)p.Hkv, groups = (cuuint64_t)p.page_size / 8;
@@ -200,11 +199,14 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
                folded ? fold_strides : strides, folded ? fold_box : box, estr5, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return ATTN_ERR_CUDA;
-    const attn_status_t st = launch_behind(paged_tiles_kernel<kF16, kD>, dim3(sms), attn::kThreads, T::kSmemBytes, stream,
-                                           tm[0], tm[1], tm[2], p, sp, tp);
+    auto kernel = paged_tiles_kernel<kF16, kD, false>;
+    if constexpr (kD == 128)
+        if (folded) kernel = paged_tiles_kernel<kF16, kD, true>;
+    const attn_status_t st =
+        launch_behind(kernel, dim3(sms), attn::kThreads, T::kSmemBytes, stream, tm[0], tm[1], tm[2], p, sp, tp);
     if (st != ATTN_OK) return st;
-    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>,
-                         dim3(sms, T::kRows / (kCombineThreads / (kD / 4))), kCombineThreads, 0, stream, p, sp);
+    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>, dim3(sms, kCombineSplit<kD, T::kRows>),
+                         kCombineThreads, 0, stream, p, sp);
 }
 
 // The rows kernel's variant for sequences of at most `rows` rows.

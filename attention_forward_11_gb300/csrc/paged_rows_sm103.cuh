@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
     using G = RowsGeo<kD, kNB>;
     constexpr int kKS = G::kKS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_part[2 * G::kWarps];
+    __shared__ long long s_part[3 * G::kWarps];
     __shared__ StartPos s_start;
     __shared__ uint32_t s_valid[G::kWarps][G::kStages];  // keys of a slice that have a page
     __shared__ int s_last;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
     wait_for_primary();
 
     typename G::ShareT sh;
-    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare>(p, sp, s_part, &s_start, sh);
+    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare, false>(p, sp, s_part, &s_start, sh);
     if (!some) return;
     typename G::CursorT cur;
     cur.first(p, sp, sh, s_start);

@@ -125,6 +125,7 @@ struct Share {
     long long begin, end;  // stretch of this block
     long long total;
     int blocks;            // that have a share
+    bool whole;            // nothing is cut: a unit counts one, and block c takes unit c
 
     // Tile at which a cut at length `at` of a unit of `tiles` tiles falls.
     __device__ __forceinline__ static int cut(long long at, int tiles) {
@@ -168,71 +169,99 @@ __device__ __forceinline__ long long block_sum(long long v, long long* part) {
     return v;
 }
 
-// The share of block blockIdx.x and the sequence it starts in (block-wide; `part`, two
+// The share of block blockIdx.x and the sequence it starts in (block-wide; `part`, three
 // values a warp, and `found` are shared scratch).  Returns false for a block without work.
-template <int kThreads, class ShareT, int kTile, int kMinShare>
+constexpr int kCutTiles = 8;  // key tiles that take as long as a cut unit's end
+
+template <int kThreads, class ShareT, int kTile, int kMinShare, bool kAlign>
 __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedParams& sp, long long* part, StartPos* found,
                                            ShareT& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreads / 32;
     const bool one_step = p.n_seqs <= kThreads;
-    long long n_units = 0;
+    long long total = 0, n_units = 0, longest = 0;
     if (!one_step) {
-        long long sum = 0;
         for (int s = tid; s < p.n_seqs; s += kThreads) {
             const Seq x = seq_of(p, s);
-            sum += seq_length(p, sp, x);
+            total += seq_length(p, sp, x);
             n_units += row_units(sp, x);
+            if (x.q_len > 0) longest = max(longest, (long long)x.kv_len);
         }
-        sh.total = block_sum<kThreads>(sum, part);
+        total = block_sum<kThreads>(total, part);
         n_units = block_sum<kThreads>(n_units, part);
+        longest = __reduce_max_sync(0xffffffffu, static_cast<int>(longest));
+        if (lane == 0) part[warp] = longest;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) longest = max(longest, part[w]);
+        __syncthreads();
     }
-    long long at = 0;  // before the step's sequences
+    long long at = 0, units_at = 0;  // before the step's sequences
     for (int s0 = 0; s0 < p.n_seqs; s0 += kThreads) {
         const int s = s0 + tid;
         Seq x{};
         if (s < p.n_seqs) x = seq_of(p, s);
         const long long len = seq_length(p, sp, x);
+        const int units = row_units(sp, x);
         long long v = len;
+        int u = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += u;
+            const long long pv = __shfl_up_sync(0xffffffffu, v, d);
+            const int pu = __shfl_up_sync(0xffffffffu, u, d);
+            if (lane >= d) v += pv, u += pu;
         }
-        if (lane == 31) part[warp] = v;
-        if (s0 == 0 && one_step) {
-            const int units = __reduce_add_sync(0xffffffffu, row_units(sp, x));
-            if (lane == 0) part[kThreads / 32 + warp] = units;
+        const int most = __reduce_max_sync(0xffffffffu, x.q_len > 0 ? x.kv_len : 0);
+        if (lane == 31) {
+            part[warp] = v;
+            part[kWarps + warp] = u;
+            part[2 * kWarps + warp] = most;
         }
         __syncthreads();
-        long long before = at, step = 0;
+        long long before = at, step = 0, units_before = units_at, units_step = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += part[w];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += part[w], units_before += part[kWarps + w];
             step += part[w];
-            if (s0 == 0 && one_step) n_units += part[kThreads / 32 + w];
+            units_step += part[kWarps + w];
+            if (one_step) longest = max(longest, part[2 * kWarps + w]);
         }
         if (s0 == 0) {
-            if (one_step) sh.total = step;
-            if (sh.total == 0) return false;
-            // a block for every unit, and more where that leaves shares of kMinShare tiles (but
-            // not a few more, which would cut every unit for little)
+            if (one_step) total = step, n_units = units_step;
+            if (total == 0) return false;
             n_units *= sp.map.head_units;
-            const long long most = sh.total / (kTile * kMinShare);
-            sh.blocks = static_cast<int>(min((long long)gridDim.x, 2 * most >= 3 * n_units ? most : n_units));
-            const long long c = blockIdx.x;
+            const long long c = blockIdx.x, G = gridDim.x;
+            // Whole units where the longest is no longer than an equal share and what a cut
+            // costs at its end (kCutTiles), or, where units share K/V tiles in L2 (kAlign: they
+            // all start at key 0 and keep in step), than 1.35 shares.
+            const long long share = quotient(total, G);
+            longest += kUnitKeys;
+            sh.whole = n_units <= G && (longest <= share + kCutTiles * kTile || (kAlign && longest * 100 <= share * 135));
+            if (sh.whole) {
+                sh.total = n_units;
+                sh.blocks = static_cast<int>(n_units);
+            } else {
+                // a block for every unit, and more where that leaves shares of kMinShare tiles
+                // (but not a few more, which would cut every unit for little)
+                sh.total = total;
+                const long long most_blocks = quotient(total, kTile * kMinShare);
+                sh.blocks = static_cast<int>(min(G, 2 * most_blocks >= 3 * n_units ? most_blocks : n_units));
+            }
             if (c >= sh.blocks) return false;
             sh.begin = quotient(c * sh.total, sh.blocks);
             sh.end = quotient((c + 1) * sh.total, sh.blocks);
         }
-        const long long end = before + v, start = end - len;
+        const long long end = sh.whole ? (units_before + u) * sp.map.head_units : before + v;
+        const long long start = end - (sh.whole ? (long long)units * sp.map.head_units : len);
         if (sh.begin >= start && sh.begin < end) {
             found->seq = s;
             found->seq_at = start;
             found->x = x;
         }
         at += step;
+        units_at += units_step;
         __syncthreads();
-        if (at > sh.begin) break;
+        if ((sh.whole ? units_at * sp.map.head_units : at) > sh.begin) break;
     }
     return true;
 }
@@ -246,6 +275,7 @@ struct Cursor {
     int tiles;        // of the whole unit, at least one
     int tile, tile_end;  // of this block's piece
     long long at, length;  // the unit's position and length
+    bool whole_units;
     bool ok;
 
     __device__ __forceinline__ bool whole() const { return tile == 0 && tile_end == tiles; }
@@ -262,6 +292,7 @@ struct Cursor {
         keys = unit_keys(p, sp, x, row_unit);
         tiles = max((keys + kTile - 1) / kTile, 1);
         length = keys + kUnitKeys;
+        if (whole_units) length = 1;
     }
     // This block's piece of the unit; false if it has none.
     __device__ __forceinline__ bool piece(const ShareT& sh) {
@@ -296,7 +327,8 @@ struct Cursor {
         x = f.x;
         ok = true;
         n_row_units = row_units(sp, x);
-        const long long per_head = units_length(p, sp, x, n_row_units);
+        whole_units = sh.whole;
+        const long long per_head = sh.whole ? n_row_units : units_length(p, sp, x, n_row_units);
         head_unit = static_cast<int>(quotient(sh.begin - f.seq_at, per_head));
         const long long head_at = f.seq_at + head_unit * per_head, rest = sh.begin - head_at;
         // the last row unit that starts at or before the position: the warp's lanes try 32 at
@@ -305,13 +337,13 @@ struct Cursor {
         int lo = 0, n = n_row_units;  // it is one of [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32, at_lane = lo + lane * step;
-            const bool before = lane * step < n && units_length(p, sp, x, at_lane) <= rest;  // lane 0: true
+            const bool before = lane * step < n && (sh.whole ? at_lane : units_length(p, sp, x, at_lane)) <= rest;  // lane 0: true
             const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
             n = min(step, n - k * step);
             lo += k * step;
         }
         row_unit = lo;
-        at = head_at + units_length(p, sp, x, lo);
+        at = head_at + (sh.whole ? lo : units_length(p, sp, x, lo));
         seek(p, sp, sh);
     }
 };
@@ -367,11 +399,15 @@ __device__ __forceinline__ bool count_piece(unsigned long long* word, int n) {
 }
 
 // Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, the
-// sums in the order of the pieces.  Grid (G, kRows / rows of a block): block (c, y) has rows
-// of the unit that block c of the first kernel starts, kD / 4 threads a row with four columns
-// each.  Most units have two or three pieces, so what the kernel costs is its instructions a
-// row and how soon its loads start: those of the first kFly pieces do not wait for M.
+// sums in the order of the pieces.  Grid (G, kCombineSplit): block (c, y) has a part of the
+// rows of the unit that block c of the first kernel starts, kD / 4 threads a row with four
+// columns each.  Most units have two or three pieces, so what the kernel costs is its
+// instructions a row and how many loads wait on one another: those of the first kFly pieces
+// are in flight before M is known, and a thread has one row (with four rows a thread and an
+// eighth of the blocks a chunk of 64 tokens on 16000 took 48 instead of 38 us).
 constexpr int kCombineThreads = 256;
+template <int kD, int kRows>
+constexpr int kCombineSplit = kRows / (kCombineThreads / (kD / 4));
 
 template <bool kF16, int kD, int kRows, int kTokenTiles>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __grid_constant__ PagedParams p,
@@ -386,28 +422,29 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
     if (h.n == 0) return;
     const int col = threadIdx.x % kLanes * 4;
     const int r = blockIdx.y * (kCombineThreads / kLanes) + threadIdx.x / kLanes;  // row of the unit
-    const size_t tail = (size_t)(2 * c + 1) * kRows + r, head = (size_t)(2 * c) * kRows + r;  // of pieces 0 and i > 0
-    auto row_of_piece = [&](int i) { return i == 0 ? tail : head + (size_t)(2 * i) * kRows; };
-    float2 ml[kFly];
-    float4 v[kFly];
-#pragma unroll
-    for (int j = 0; j < kFly; ++j) {
-        ml[j] = make_float2(-INFINITY, 0.f);
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
     const Seq x = seq_of(p, h.seq);
     const int tile_tokens = sp.map.tokens / kTokenTiles, tile = r / kTileRows;
     const Row w = row_of(p, sp.map, x, h.head_unit, h.row_unit * sp.map.tokens + tile * tile_tokens, tile_tokens,
                          r % kTileRows);
     if (!w.there) return;
+    // row of the workspace that holds piece i
+    auto ws_row = [&](int i) { return (size_t)piece_slot(c, i) * kRows + r; };
+    float2 ml[kFly];
+    float4 v[kFly];
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < kFly; ++j)
-        if (j < h.n) {
-            ml[j] = sp.ws.ml[row_of_piece(j)];
-            v[j] = *reinterpret_cast<const float4*>(sp.ws.o + row_of_piece(j) * kD + col);
+        for (int j = 0; j < kFly; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + j < h.n) {
+                ml[j] = sp.ws.ml[ws_row(i0 + j)];
+                v[j] = *reinterpret_cast<const float4*>(sp.ws.o + ws_row(i0 + j) * kD + col);
+            }
         }
+    };
+    load(0);
     float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    for (int i = kFly; i < h.n; ++i) M = fmaxf(M, sp.ws.ml[row_of_piece(i)].x);
+    for (int i = kFly; i < h.n; ++i) M = fmaxf(M, sp.ws.ml[ws_row(i)].x);
     const float use = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -423,15 +460,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
         }
         i0 += kFly;
         if (i0 >= h.n) break;
-#pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-            ml[j] = make_float2(-INFINITY, 0.f);
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + j < h.n) {
-                ml[j] = sp.ws.ml[row_of_piece(i0 + j)];
-                v[j] = *reinterpret_cast<const float4*>(sp.ws.o + row_of_piece(i0 + j) * kD + col);
-            }
-        }
+        load(i0);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t tok = (size_t)x.q0 + w.token;

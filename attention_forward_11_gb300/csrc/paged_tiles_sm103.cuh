@@ -23,6 +23,7 @@
 #pragma once
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 
 #include "fmha_fwd_sm103.cuh"
@@ -37,6 +38,12 @@ constexpr int kSchedWarp = kMmaWarp + 3;
 constexpr int kItems = 4;       // work items posted ahead
 constexpr int kMaskRing = 8;    // page masks of the last K tiles
 constexpr int kItemReaders = kSoftmaxWarps + 4 + 2;  // warps that read an item
+
+// Registers a thread, of the launch's 4 x 128: the epilogue's row addresses take more than
+// the dense forward's, its softmax can spare them (no spills at head size 128).
+constexpr int kTilesRegsSoftmax = 168, kTilesRegsEpilogue = 96, kTilesRegsOther = 80;
+static_assert(2 * kTilesRegsSoftmax + kTilesRegsEpilogue + kTilesRegsOther <= 4 * (65536 / kThreads),
+              "register split exceeds the launch allocation");
 
 struct Item {
     int seq, q0, q_len, kv_len;  // the sequence
@@ -89,7 +96,7 @@ struct TilesGeo {
     static constexpr int kSmemMask = kSmemMmaExit + 4;
     static constexpr int kSmemStart = (kSmemMask + kMaskRing * 4 + 7) / 8 * 8;
     static constexpr int kSmemPart = kSmemStart + static_cast<int>(sizeof(StartPos));
-    static constexpr int kSmemItems = kSmemPart + 2 * (kThreads / 32) * 8;
+    static constexpr int kSmemItems = kSmemPart + 3 * (kThreads / 32) * 8;
     static constexpr int kSmemUsed = kSmemItems + kItems * static_cast<int>(sizeof(Item));
     static constexpr int kSmemBytes = kSmemUsed + 1024;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
@@ -98,13 +105,6 @@ struct TilesGeo {
 
 struct TilesParams {
     int box_rows;   // rows of a K/V box: gcd(page_size, 128)
-    // A K/V tile in shared memory: 8-row groups of 128-byte rows, `group_bytes` apart, and
-    // the second 64 columns (head size 128) `half_bytes` behind the first.  Copied half by
-    // half, the halves are 16 KB blocks (1024 and 16384).  Where the cache's strides let
-    // a tensor map step over a row's two halves inside a group (paged_api.cuh), one box has
-    // both, and the groups of the halves alternate (2048 and 1024): half the copies.
-    int half_bytes, group_bytes;
-    int halves;          // halves that are copied apart: 2 or 1
     int head_at_half;    // coordinates of a folded box: third = head * head_at_half,
     int head_at_group;   // fourth = head * head_at_group + row / 8
     int tile_tokens;  // tokens of a row tile
@@ -131,13 +131,20 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
-template <bool kF16, int kD>
+// kFold: one box has both 64-column halves of head size 128.  A K/V tile in shared memory
+// is 8-row groups of 128-byte rows, kKvGroup bytes apart, the second half's columns kKvHalf
+// behind the first's.  Copied half by half the halves are 16 KB blocks; in one box, where the
+// cache's strides let a tensor map step over a row's halves inside a group (paged_api.cuh),
+// the groups of the halves alternate, and a tile takes half the copies.
+template <bool kF16, int kD, bool kFold>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p,
                        const __grid_constant__ SchedParams sp, const __grid_constant__ TilesParams tp) {
     using T = TilesGeo<kD>;
     constexpr int kStages = T::kStages;
+    constexpr int kBoxHalves = kFold ? 1 : T::kHalves;  // halves that are copied apart
+    constexpr int kKvHalf = kFold ? 1024 : kHalfBytes, kKvGroup = kFold ? 2048 : 1024;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_for_primary();
     typename T::ShareT sh;
     if (threadIdx.x == 0) sp.ws.header[blockIdx.x].n = 0;
-    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare>(
+    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare, true>(
             p, sp, reinterpret_cast<long long*>(smem + T::kSmemPart), start, sh)) {
         if (warp == 0) tmem_dealloc(tmem_base, kTmemCols);
         return;
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (wg == 3) {
-      regs_dec<kRegsOther>();
+      regs_dec<kTilesRegsOther>();
       if (warp == kSchedWarp) {
         // =========================== work items ============================
         typename T::CursorT cur;
@@ -294,11 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile, half (lane % 16) % halves of its columns.
         const uint64_t pol_q = l2_policy_evict_first();
         const uint64_t pol_kv = l2_policy_evict_last();
-        const int box = (lane & 15) / tp.halves, half = (lane & 15) % tp.halves;
-        const bool folded = tp.halves < T::kHalves;
+        const int box = (lane & 15) / kBoxHalves, half = (lane & 15) % kBoxHalves;
         const int n_boxes = kBM / tp.box_rows;
         const bool copies = box < n_boxes;
-        const uint32_t box_at = half * kHalfBytes + box * (tp.box_rows / 8) * tp.group_bytes;
+        const uint32_t box_at = half * kHalfBytes + box * (tp.box_rows / 8) * kKvGroup;
         int g = 0;                       // stages issued
         int q_issued[kTiles] = {0, 0};   // Q_t fills posted so far
         bool ok = true;
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t mask = 0;  // one bit per 16 keys
                     const int per = tp.box_rows / 16;
                     for (int b = 0; miss != 0 && b < n_boxes; ++b)
-                        if ((miss >> (b * tp.halves)) & 1) mask |= ((1u << per) - 1u) << (b * per);
+                        if ((miss >> (b * kBoxHalves)) & 1) mask |= ((1u << per) - 1u) << (b * per);
                     page_mask[g % kMaskRing] = mask;
                 }
                 mbar_arrive_expect_tx(bar(T::kBarKvFull + st), ((have_k ? 1 : 0) + (have_v ? 1 : 0)) * T::kTileBytes);
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                            : T::kSmemV + ((g - 1) % kStages) * T::kTileBytes);
                 const CUtensorMap* map = is_k ? &tm_k : &tm_v;
                 const int hkv = is_k ? k_hkv : v_hkv, row = is_k ? k_row : v_row, pg = is_k ? k_page : v_page;
-                if (folded)
+                if constexpr (kFold)
                     tma_load_5d(to, map, 0, 0, hkv * tp.head_at_half, hkv * tp.head_at_group + row / 8, pg,
                                 bar(T::kBarKvFull + st), pol_kv);
                 else
@@ -408,10 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_qk = idesc_f16kind_f32(kBM, kBN, false, kF16);
         constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kD, true, kF16);
         const uint64_t q_desc0 = sdesc_sw128(sbase + T::kSmemQ, 16, 1024);
-        const uint64_t k_desc0 = sdesc_sw128(sbase + T::kSmemK, 16, tp.group_bytes);
-        const uint64_t v_desc0 = sdesc_sw128(sbase + T::kSmemV, tp.half_bytes, tp.group_bytes);
-        const uint64_t k_half = static_cast<uint64_t>(tp.half_bytes >> 4);   // K: to its second half's columns
-        const uint64_t v_step = static_cast<uint64_t>(tp.group_bytes >> 3);  // V: 16 keys = two groups
+        const uint64_t k_desc0 = sdesc_sw128(sbase + T::kSmemK, 16, kKvGroup);
+        const uint64_t v_desc0 = sdesc_sw128(sbase + T::kSmemV, kKvHalf, kKvGroup);
         auto issue_qk = [&](int t, int ks) {
             const uint32_t d = tmem_base + kTmemS + 128 * t;
             const uint64_t qd = q_desc0 + static_cast<uint64_t>((t * T::kTileBytes) >> 4);
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk) {
                 const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
-                mma_bf16_ss(d, qd + off, kd + (kk >> 2) * k_half + static_cast<uint64_t>((kk & 3) * 2), idesc_qk,
+                mma_bf16_ss(d, qd + off, kd + static_cast<uint64_t>(((kk >> 2) * kKvHalf + (kk & 3) * 32) >> 4), idesc_qk,
                             kk > 0 ? 1u : 0u);
             }
         };
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < kBN / 32; ++q) {
                 const int kk = h * (kBN / 32) + q;
-                mma_bf16_ts(d, pa + kk * 8, vd + kk * v_step, idesc_pv,
+                mma_bf16_ts(d, pa + kk * 8, vd + static_cast<uint64_t>((kk * 2 * kKvGroup) >> 4), idesc_pv,
                             (accumulate || kk > 0) ? 1u : 0u);
             }
         };
@@ -457,71 +461,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && elect_one()) mma_commit(bar(T::kBarKvEmpty));  // stage 0 holds K_0 alone
             __syncwarp();
         }
+        Item wn;
+        bool have_n = false;
+        // Step kt of item j.  The last step of an item is code of its own and the tiles are
+        // unrolled: the loop over the others stays a straight run of MMAs (2900 to 2700
+        // cycles a step).
+        auto step = [&](auto last_step, int j, int kt) -> bool {
+            constexpr bool kLast = decltype(last_step)::value;
+            const int vs = kv % kStages;
+            const int kn = kv + 1;  // stage kn: V_{kt} and K_{kt+1} (or the next item's K_0)
+            if constexpr (kLast) {
+                have_n = get_item(j + 1, wn, ok);
+                if (!ok) return false;
+            }
+            if (!wait_bounded(bar(T::kBarKvFull + kn % kStages), (kn / kStages) & 1, abort_flag, limit)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int nt = w.n(t);
+                if (kt < nt) {
+                    // the first P.V of a unit overwrites O_t: the previous unit's
+                    // epilogue must have read it out of tensor memory
+                    if (kt == 0 && j > 0 && !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit))
+                        return false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        named_bar_sync(kBarP + 2 * t + h, kBarPThreads);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_pv(t, vs, h, kt > 0);
+                            if (h == 1 && kt == nt - 1) mma_commit(bar(T::kBarODone + t));  // O_t final
+                        }
+                        __syncwarp();
+                    }
+                } else if (nt == 0 && kt == 0) {
+                    // tile without work: its (all-zero) O_t is "final" once the previous
+                    // unit's was read, which keeps the barrier in step with the epilogue
+                    if (j > 0 && !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit)) return false;
+                    if (elect_one()) mma_commit(bar(T::kBarODone + t));
+                    __syncwarp();
+                }
+                if constexpr (kLast) {
+                    // the next item's S_t(0), before the other tile's last P.V: its softmax
+                    // starts while this item ends
+                    if (have_n && !first_s(j + 1, wn, t, kn % kStages)) return false;
+                } else if (kt + 1 < nt) {
+                    if (elect_one()) {
+                        issue_qk(t, kn % kStages);
+                        mma_commit(bar(T::kBarSFull + t));
+                        if (kt + 2 == nt) mma_commit(bar(T::kBarQEmpty + t));  // last S_t of the unit
+                    }
+                    __syncwarp();
+                }
+            }
+            // stage kn is free once its V and its K have been read
+            if ((!kLast || have_n) && elect_one()) mma_commit(bar(T::kBarKvEmpty + kn % kStages));
+            __syncwarp();
+            ++kv;
+            return true;
+        };
         for (int j = 0; ok && have; ++j) {
             const int nm = w.nmax();
-            Item wn;
-            bool have_n = false;
-            for (int kt = 0; ok && kt < nm; ++kt) {
-                const int vs = kv % kStages;
-                const int kn = kv + 1;  // stage kn: V_{kt} and K_{kt+1} (or the next item's K_0)
-                const bool last = kt + 1 == nm;
-                if (last) have_n = get_item(j + 1, wn, ok);
-                if (!ok || !wait_bounded(bar(T::kBarKvFull + kn % kStages), (kn / kStages) & 1, abort_flag, limit)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                for (int t = 0; t < kTiles; ++t) {
-                    const int nt = w.n(t);
-                    if (kt < nt) {
-                        // the first P.V of a unit overwrites O_t: the previous unit's
-                        // epilogue must have read it out of tensor memory
-                        if (kt == 0 && j > 0 &&
-                            !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        for (int h = 0; h < 2; ++h) {
-                            named_bar_sync(kBarP + 2 * t + h, kBarPThreads);
-                            tc_fence_after();
-                            if (elect_one()) {
-                                issue_pv(t, vs, h, kt > 0);
-                                if (h == 1 && kt == nt - 1) mma_commit(bar(T::kBarODone + t));  // O_t final
-                            }
-                            __syncwarp();
-                        }
-                    } else if (nt == 0 && kt == 0) {
-                        // tile without work: its (all-zero) O_t is "final" once the previous
-                        // unit's was read, which keeps the barrier in step with the epilogue
-                        if (j > 0 && !wait_bounded(bar(T::kBarOFree + t), (j - 1) & 1, abort_flag, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        if (elect_one()) mma_commit(bar(T::kBarODone + t));
-                        __syncwarp();
-                    }
-                    if (kt + 1 < nt) {
-                        if (elect_one()) {
-                            issue_qk(t, kn % kStages);
-                            mma_commit(bar(T::kBarSFull + t));
-                            if (kt + 2 == nt) mma_commit(bar(T::kBarQEmpty + t));  // last S_t of the unit
-                        }
-                        __syncwarp();
-                    } else if (last && have_n) {
-                        // the next item's S_t(0), before the other tile's last P.V: its
-                        // softmax starts while this item ends
-                        if (!first_s(j + 1, wn, t, kn % kStages)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                }
-                if (!ok) break;
-                // stage kn is free once its V and its K have been read
-                if ((!last || have_n) && elect_one()) mma_commit(bar(T::kBarKvEmpty + kn % kStages));
-                __syncwarp();
-                ++kv;
-            }
+            for (int kt = 0; ok && kt + 1 < nm; ++kt) ok = step(std::false_type{}, j, kt);
+            if (ok) ok = step(std::true_type{}, j, nm - 1);
             have = have_n;
             w = wn;
         }
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (wg < 2) {
         // =========================== softmax warpgroups =====================
-        regs_inc<kRegsSoftmax>();
+        regs_inc<kTilesRegsSoftmax>();
         const int t = warp / 4;
         const int wq = warp % 4;
         const int r = wq * 32 + lane;  // row within the tile = TMEM lane
@@ -566,21 +568,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok; ++j) {
             Item w;
             if (!get_item(j, w, ok)) break;
-            const int nt = w.n(t);
+            const int nt = w.n(t), nm = w.nmax();
             const int token = w.t0 + t * tp.tile_tokens + row_token;
-            int lim = -1;  // last visible key
+            int nvis = 0;  // visible keys of this row from the item's next key tile on
             if (row_token < tp.tile_tokens && token < w.q_len)
-                lim = (p.causal ? max(w.kv_len - w.q_len + token + 1, 0) : w.kv_len) - 1;
+                nvis = (p.causal ? max(w.kv_len - w.q_len + token + 1, 0) : w.kv_len) - w.kb * kBN;
+            // keys of the sequence in its last tile, and which of the item's tiles that is
+            // (past the last: the item does not reach it, or it is full)
+            const int last_kt = w.kv_len % kBN != 0 ? w.kv_len / kBN - w.kb : 0x7fffffff;
+            const int last_keys = w.kv_len % kBN;
             float m_run = -INFINITY;  // running max (log2 units of scaled logits) used by the weights
             float l_run = 0.f;        // running sum of weights
 
-            for (int kt = 0; kt < nt; ++kt, ++sc) {
+            for (int kt = 0; kt < nt; ++kt, ++sc, nvis -= kBN) {
                 const bool got = wait_bounded(bar(T::kBarSFull + t), sc & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t missing = page_mask[(kv + kt) % kMaskRing];
                 uint32_t s[128];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -588,20 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
 
-                const int key0 = (w.kb + kt) * kBN;
-                const int nvis = lim - key0 + 1;  // visible keys of this row in the tile
                 if (nvis < kBN) {
 #pragma unroll
                     for (int jj = 0; jj < kBN; ++jj)
                         if (jj >= nvis) s[jj] = __float_as_uint(-INFINITY);
                 }
-                const uint32_t missing = page_mask[(kv + kt) % kMaskRing];
                 if (missing != 0) {  // keys without a page
 #pragma unroll
                     for (int jj = 0; jj < kBN; ++jj)
                         if ((missing >> (jj / 16)) & 1) s[jj] = __float_as_uint(-INFINITY);
                 }
-                if (w.kv_len - key0 < kBN) {
+                if (kt == last_kt) {
                     // V's rows behind the last key become zero.  V_kt lands with stage kv + kt + 1,
                     // which is not refilled before this tile's weights have been used.
                     const int sn = kv + kt + 1;
@@ -611,10 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     uint8_t* v = smem + T::kSmemV + ((kv + kt) % kStages) * T::kTileBytes;
-                    const int first = (w.kv_len - key0) * 8;  // 16-byte pieces of a half, 64 a group
+                    const int first = last_keys * 8;  // 16-byte pieces of a half, 64 a group
                     for (int h = 0; h < T::kHalves; ++h)
                         for (int i = first + r; i < kBN * 8; i += 128)
-                            *reinterpret_cast<uint4*>(v + h * tp.half_bytes + (i >> 6) * tp.group_bytes + (i & 63) * 16) =
+                            *reinterpret_cast<uint4*>(v + h * kKvHalf + (i >> 6) * kKvGroup + (i & 63) * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l_run = l_run * alpha + ((rs0 + rs1) + (rs2 + rs3));
             }
             if (!ok) break;
-            kv += w.nmax();
+            kv += nm;
 
             // hand (m, l) of every row to the epilogue warpgroup and start the next unit
             const bool got = j == 0 || wait_bounded(bar(T::kBarStatsFree + t), (j - 1) & 1, abort_flag, limit);
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // =========================== epilogue warpgroup =====================
-        regs_dec<kRegsEpilogue>();
+        regs_dec<kTilesRegsEpilogue>();
         const int wq = warp % 4;
         const int r = wq * 32 + lane;  // row within a tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
