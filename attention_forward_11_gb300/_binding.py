@@ -290,9 +290,20 @@ def attn_bwd(q, k, v, o, lse, do, causal: int = 0, scale: float | None = None, d
 # ---- paged key/value cache
 
 # A step of a server makes dozens of these calls, some of a few microseconds on the GPU, so
-# the checks read each property once and nothing is allocated that the caller passed.
+# the checks read each property once, in one expression, and only a call that fails them
+# looks for the reason.
 
-def _on_one_gpu(tensors) -> int:
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _on_one_gpu(*tensors) -> int:
     """Index of the CUDA device that holds all of `tensors` (None entries aside)."""
     device = tensors[0].get_device()
     for t in tensors:
@@ -329,17 +340,6 @@ class _on:
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
-
-
-def _is_here(device: int, stream) -> bool:
-    """The common case, for which no guard is set up: the current device and stream."""
-    import torch
-    return stream is None and torch.cuda.current_device() == device
-
-
-def _current_handle(device: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device)  # current_stream(device).cuda_stream, 2 us cheaper
 
 
 def _bad(name, want):
@@ -401,23 +401,27 @@ def attn_paged_tables(ctx_lens, new_lens, free_pages, block_table, page_size: in
     [max_tokens], counts int32 [4]: new tokens, next free_head, missing pages,
     sequences longer than a table row).  Outputs are allocated here if None.
     """
-    import torch
-    device = _on_one_gpu((ctx_lens, new_lens, free_pages, block_table, free_head, cu_new, kv_lens, slot_map, counts))
-    if not _is_here(device, stream):
-        with _on(device, stream) as handle:
-            return _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens,
-                                 free_head, cu_new, kv_lens, slot_map, counts)
-    return _paged_tables(torch, _current_handle(device), ctx_lens, new_lens, free_pages, block_table, page_size,
-                         max_tokens, free_head, cu_new, kv_lens, slot_map, counts)
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(ctx_lens, new_lens, free_pages, block_table, free_head, cu_new, kv_lens, slot_map, counts)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        # the current device and stream: no guard (current_stream(device).cuda_stream costs 2 us)
+        return _paged_tables(torch, torch._C._cuda_getCurrentRawStream(device), ctx_lens, new_lens, free_pages,
+                             block_table, page_size, max_tokens, free_head, cu_new, kv_lens, slot_map, counts)
+    with _on(device, stream) as handle:
+        return _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_head,
+                             cu_new, kv_lens, slot_map, counts)
 
 
 def _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, page_size, max_tokens, free_head, cu_new,
                   kv_lens, slot_map, counts):
     i32 = torch.int32
     n, n_free, max_tokens = ctx_lens.numel(), free_pages.numel(), int(max_tokens)
-    _check_ints("ctx_lens", ctx_lens, i32, n)
-    _check_ints("new_lens", new_lens, i32, n)
-    _check_ints("free_pages", free_pages, i32, n_free)
+    if not (ctx_lens.dtype is i32 and new_lens.dtype is i32 and free_pages.dtype is i32 and ctx_lens.dim() == 1 and
+            new_lens.dim() == 1 and free_pages.dim() == 1 and new_lens.numel() == n and ctx_lens.is_contiguous() and
+            new_lens.is_contiguous() and free_pages.is_contiguous()):
+        _check_ints("ctx_lens", ctx_lens, i32, n)
+        _check_ints("new_lens", new_lens, i32, n)
+        _check_ints("free_pages", free_pages, i32, n_free)
     if free_head is not None:
         _check_ints("free_head", free_head, i32, 1)
     table_stride = _table_stride(block_table, n, i32)
@@ -451,8 +455,8 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
     """Write the rows of k and v ([T, Hkv, D], heads contiguous, any row stride) into
     slots slot_map[t] (int64 [T], rows outside the cache skipped) of k_cache and v_cache
     ([n_pages, page_size, Hkv, D], any strides with D contiguous), in place."""
-    import torch
-    device = _on_one_gpu((k, v, slot_map, k_cache, v_cache))
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(k, v, slot_map, k_cache, v_cache)
     _check_cache(k_cache, v_cache, "k, v", k.dtype, (torch.bfloat16, torch.float16))
     n_pages, page_size, Hkv, D = k_cache.shape
     T = k.shape[0]
@@ -462,8 +466,8 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
     ps, ts, hs, _ = k_cache.stride()
     args = (k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, D, n_pages,
             page_size, _row_stride("k", k, Hkv, D), _row_stride("v", v, Hkv, D), ps, ts, hs)
-    if _is_here(device, stream):
-        st = attn_paged_append_ptr(*args, _current_handle(device))
+    if stream is None and torch._C._cuda_getDevice() == device:
+        st = attn_paged_append_ptr(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with _on(device, stream) as handle:
             st = attn_paged_append_ptr(*args, handle)
@@ -493,14 +497,14 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: i
     rows of no sequence are left as they were.  `workspace`: a CUDA byte tensor of at least
     attn_paged_fwd_workspace_size(...) bytes; it and the outputs are allocated here if None.
     """
-    import torch
-    device = _on_one_gpu((q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse, workspace))
-    if not _is_here(device, stream):
-        with _on(device, stream) as handle:
-            return _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o,
-                              lse, workspace, want_lse)
-    return _paged_fwd(torch, _current_handle(device), q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal,
-                      scale, o, lse, workspace, want_lse)
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(q, k_cache, v_cache, block_table, cu_q, kv_lens, o, lse, workspace)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return _paged_fwd(torch, torch._C._cuda_getCurrentRawStream(device), q, k_cache, v_cache, block_table, cu_q,
+                          kv_lens, max_q_len, causal, scale, o, lse, workspace, want_lse)
+    with _on(device, stream) as handle:
+        return _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o,
+                          lse, workspace, want_lse)
 
 
 def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o, lse, workspace,
