@@ -64,6 +64,9 @@ class Batch:
             c = [torch.empty(n, page, H, D, dtype=self.dtype, device=self.device) for _ in range(2)]
         elif layout == "heads":
             c = [torch.empty(n, H, page, D, dtype=self.dtype, device=self.device).transpose(1, 2) for _ in range(2)]
+        elif layout == "wide":  # a head's K and V side by side: heads 2 D apart
+            x = torch.empty(n, page, H, 2 * D, dtype=self.dtype, device=self.device)
+            c = [x[..., :D], x[..., D:]]
         else:  # K and V in turn
             x = torch.empty(n, 2, page, H, D, dtype=self.dtype, device=self.device)
             c = [x[:, 0], x[:, 1]]

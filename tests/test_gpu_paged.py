@@ -150,6 +150,92 @@ def test_fwd(name, Hq, Hkv, D, page, dtype, layout):
     check(b, o, lse, untouched=9.0)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page,layout", [
+    (4, 2, 128, 16, "wide"), (4, 2, 64, 64, "wide"), (4, 2, 128, 128, "wide"),   # heads 2 D apart
+    (48, 1, 64, 7, "tokens"), (80, 2, 128, 1, "heads"),                             # groups past a block's rows
+    (160, 1, 64, 16, "tokens"), (140, 1, 128, 32, "turns"), (50, 1, 256, 16, "tokens")])
+@pytest.mark.parametrize("lens", [[(130, 1), (17, 1), (400, 1)], [(200, 70), (33, 5), (300, 1)]], ids=["decode", "chunk"])
+def test_fwd_wide_rows_and_groups(lens, Hq, Hkv, D, page, layout):
+    b = Batch(lens, Hq, Hkv, D, page, layout=layout, pad_rows=1, seed=Hq)
+    check(b, *run_fwd(b), untouched=9.0)
+
+
+@pytest.mark.parametrize("n", [257, 700])
+@pytest.mark.parametrize("kind", ["decode", "chunks", "mixed"])
+def test_fwd_many_sequences(n, kind):
+    """More sequences than a block has threads: the lengths are read in several steps."""
+    rng = random.Random(n)
+    lens = []
+    for i in range(n):
+        q = {"decode": 1, "chunks": rng.randint(1, 40), "mixed": 200 if i % 97 == 5 else 1}[kind]
+        q = 0 if rng.random() < 0.1 else q
+        lens.append((q + rng.randint(0, 60), q))
+    b = Batch(lens, 4, 2, 64, 16, seed=n)
+    check(b, *run_fwd(b))
+    if kind == "decode":
+        b = Batch(lens, 2, 1, 256, 16, seed=n)
+        check(b, *run_fwd(b))
+
+
+def test_fwd_one_long_sequence_among_many():
+    """Shares that cut one unit many times and take others whole."""
+    lens = [(30000, 1)] + [(rng, 1) for rng in range(1, 200)]
+    b = Batch(lens, 4, 1, 64, 16, seed=3)
+    check(b, *run_fwd(b))
+    lens = [(30000, 40), (3, 3)] + [(100 + i, 50) for i in range(30)]
+    b = Batch(lens, 2, 1, 64, 16, seed=3)
+    check(b, *run_fwd(b))
+
+
+@pytest.mark.parametrize("lens,max_q", [([(20000, 1), (9000, 1), (40, 1)], 1), ([(20000, 100), (300, 1), (8000, 1)], 100)],
+                         ids=["rows", "mixed"])
+def test_fwd_workspace_contents_do_not_matter(lens, max_q):
+    b = Batch(lens, 8, 1, 128, 16, seed=30)
+    a = b.on_gpu()
+    size = fa.attn_paged_fwd_workspace_size(b.T, max_q, 8, 1, 128, 16)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    first = None
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for fill in ("zero", "ones", "random", "nan", "as left", "as left"):
+        if fill == "ones":
+            ws.fill_(255)
+        elif fill == "random":
+            ws.copy_(torch.randint(0, 256, (size,), dtype=torch.uint8, device="cuda", generator=g))
+        elif fill == "nan":
+            ws[:size // 4 * 4].view(torch.float32).fill_(float("nan"))
+        o, lse = fa.attn_paged_fwd(**a, max_q_len=max_q, workspace=ws)
+        ok()
+        if first is None:
+            first = (o, lse)
+            check(b, o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1]), fill
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed one after the other, in any order, each many times."""
+    bs = [Batch([(20000, 1), (37, 1)], 8, 1, 128, 16, seed=31), Batch([(9000, 60), (500, 1)], 8, 1, 128, 16, seed=32)]
+    size = max(fa.attn_paged_fwd_workspace_size(b.T, 60, 8, 1, 128, 16) for b in bs)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for b, max_q in zip(bs, (1, 60)):
+        a = b.on_gpu()
+        o = torch.empty_like(a["q"])
+        lse = torch.empty((8, b.q.shape[0]), dtype=torch.float32, device="cuda")
+        fa.attn_paged_fwd(**a, max_q_len=max_q, o=o, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa.attn_paged_fwd(**a, max_q_len=max_q, o=o, lse=lse, workspace=ws)
+        graphs.append((g, a))
+        outs.append((o, lse))
+    for i in (0, 0, 1, 0, 1, 1, 0):
+        outs[i][0].fill_(9.0)
+        graphs[i][0].replay()
+    ok()
+    for b, (o, lse) in zip(bs, outs):
+        check(b, o, lse)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("name", ["verify", "mixed"])
 def test_fwd_every_key_visible(name, D):
