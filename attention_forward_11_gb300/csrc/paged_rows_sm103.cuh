@@ -71,6 +71,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kN>
 __device__ __forceinline__ void cp_async_wait() {
@@ -107,11 +110,11 @@ struct RowsGeo {
 // O = sum O 2^(m - M) / L.  kD / 4 threads have a row (four columns each), or, when there are
 // fewer rows than such groups, a part of a row's pieces; `buf` is shared scratch of a row and
 // its sum for every group.  A block does this alone at its end, so what counts is how many
-// loads wait on one another: 16 pieces are in flight at once, the first before M is known.
+// loads wait on one another: 20 pieces are in flight at once, the first before M is known.
 template <bool kF16, int kD, int kRows, int kThreads>
 __device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedParams& sp, const Seq& x, int head_unit, int t0,
                                             int first, int n, float* buf) {
-    constexpr int kLanes = kD / 4, kGroups = kThreads / kLanes, kFly = 16;
+    constexpr int kLanes = kD / 4, kGroups = kThreads / kLanes, kFly = 20;
     constexpr int kSpan = kLanes < 32 ? kLanes : 32;  // lanes that share a search for M
     const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4, lane = threadIdx.x % kSpan;
     const int rows = min(min(sp.map.tokens, x.q_len - t0) * sp.map.heads, kRows);
@@ -240,7 +243,11 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
             ld_tile = ld.tile;
         }
     };
-    // Copies a slice into a stage.
+    // Copies a slice into a stage.  A lane has 16 bytes of every (32 / kChunks)-th row.
+    constexpr int kRowsAtOnce = 32 / G::kChunks, kCopies = 16 / kRowsAtOnce;  // of a 16-key block
+    const int lane_row = lane / G::kChunks, lane_chunk = lane % G::kChunks;
+    const long long lane_at = lane_row * p.token_stride + lane_chunk * 8;
+    const bool blocks_in_pages = p.page_size % 16 == 0;
     auto copy = [&](const Look& k, int st) {
         if (k.ok) {
             const bool there = k.page >= 0 && k.page < p.n_pages;
@@ -248,15 +255,30 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
             const uint32_t valid = __ballot_sync(0xffffffffu, there);
             if (lane == 0) s_valid[warp][st] = valid;
             const uint32_t to = ring + st * (2 * G::kSliceBytes);
-            if (k.some) {
+            auto place = [&](int row) { return to + row * (kD * 2) + ((lane_chunk ^ (row & 7)) << 4); };
+            if (blocks_in_pages && valid == 0xffffffffu) {
+                // 16 keys of one page each: a third of the instructions of the other way
 #pragma unroll
-                for (int i = 0; i < G::kSlice * G::kChunks / 32; ++i) {
-                    const int idx = lane + 32 * i, kk = idx / G::kChunks, ch = idx % G::kChunks;
-                    const long long at = __shfl_sync(0xffffffffu, base, kk) + ch * 8;
-                    const bool ok = (valid >> kk) & 1;
-                    const uint32_t dst = to + kk * (kD * 2) + ((ch ^ (kk & 7)) << 4);
-                    cp_async16(dst, p.k + at, ok);
-                    cp_async16(dst + G::kSliceBytes, p.v + at, ok);
+                for (int b = 0; b < kKS; ++b) {
+                    const long long at = __shfl_sync(0xffffffffu, base, 16 * b) + lane_at;
+                    const uint16_t *pk = p.k + at, *pv = p.v + at;
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        const uint32_t dst = place(16 * b + lane_row + i * kRowsAtOnce);
+                        cp_async16(dst, pk);
+                        cp_async16(dst + G::kSliceBytes, pv);
+                        pk += kRowsAtOnce * p.token_stride;
+                        pv += kRowsAtOnce * p.token_stride;
+                    }
+                }
+            } else if (k.some) {
+#pragma unroll
+                for (int i = 0; i < kKS * kCopies; ++i) {
+                    const int row = lane_row + i * kRowsAtOnce;
+                    const long long at = __shfl_sync(0xffffffffu, base, row) + lane_chunk * 8;
+                    const bool ok = (valid >> row) & 1;
+                    cp_async16(place(row), p.k + at, ok);
+                    cp_async16(place(row) + G::kSliceBytes, p.v + at, ok);
                 }
             }
         }
@@ -451,11 +473,11 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
                             o[nb][part * (G::kMergeCols / 16) + mt][e];
                 __syncthreads();
 #pragma unroll
-                for (int i = tid; i < 8 * (G::kMergeCols / 4); i += G::kThreads) {
-                    const int r = i / (G::kMergeCols / 4), dc = (i % (G::kMergeCols / 4)) * 4, d = part * G::kMergeCols + dc;
+                for (int i = tid; i < 8 * (G::kMergeCols / 2); i += G::kThreads) {
+                    const int r = i / (G::kMergeCols / 2), dc = (i % (G::kMergeCols / 2)) * 2, d = part * G::kMergeCols + dc;
                     const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + r);
                     if (!w.there) continue;
-                    float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+                    float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
                     for (int k = 0; k < G::kWarps; ++k) M = fmaxf(M, stats[k * G::kRows + 8 * nb + r].x);
                     const float use = M == -INFINITY ? 0.f : M;
@@ -463,26 +485,21 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
                     for (int k = 0; k < G::kWarps; ++k) {
                         const float2 ml = stats[k * G::kRows + 8 * nb + r];
                         const float f = ex2_approx(ml.x - use);
-                        const float4 v = *reinterpret_cast<const float4*>(merge + (k * 8 + r) * G::kMergeStride + dc);
+                        const float2 v = *reinterpret_cast<const float2*>(merge + (k * 8 + r) * G::kMergeStride + dc);
                         L += ml.y * f;
                         a0 += v.x * f;
                         a1 += v.y * f;
-                        a2 += v.z * f;
-                        a3 += v.w * f;
                     }
                     if (whole) {
                         const float inv = L == 0.f ? 0.f : 1.f / L;
                         const long long tok = x.q0 + w.token;
-                        uint2 out;
-                        out.x = pack_x2<kF16>(a0 * inv, a1 * inv);
-                        out.y = pack_x2<kF16>(a2 * inv, a3 * inv);
-                        *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + d) = out;
+                        *reinterpret_cast<uint32_t*>(p.o + (tok * p.Hq + w.head) * kD + d) = pack_x2<kF16>(a0 * inv, a1 * inv);
                         if (d == 0 && p.lse != nullptr)
                             p.lse[(long long)w.head * p.total_q + tok] =
                                 L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
                     } else {
                         const size_t row = (size_t)slot * G::kRows + 8 * nb + r;
-                        *reinterpret_cast<float4*>(sp.ws.o + row * kD + d) = make_float4(a0, a1, a2, a3);
+                        *reinterpret_cast<float2*>(sp.ws.o + row * kD + d) = make_float2(a0, a1);
                         if (d == 0) sp.ws.ml[row] = make_float2(M, L);
                     }
                 }
