@@ -222,12 +222,16 @@ attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows,
     return launch_rows<kF16, kD, 2>(p, workspace, sms, stream);
 }
 
-// Are there likely to be single tokens among the long sequences?  The lengths are on the
-// device; on the host the longest one against the mean tells.  A row tile of 128 with one
-// token in it costs 1.7 us a key tile however few rows it has, where the rows kernel
-// streams the cache, but the rows kernel costs 2.5 us when there is nothing for it.
-bool is_mixed(const attn::paged::PagedParams& p, int max_q_len) {
-    return p.group <= 32 && (long long)max_q_len * p.n_seqs >= 4ll * p.total_q && p.n_seqs > 1;
+// Does a batch with long sequences have so many single tokens that they are worth a kernel of
+// their own?  The lengths are on the device; on the host the longest sequence against the
+// mean tells.  A row tile with one token in it takes a key tile about as fast as the cache
+// can be read, and blocks that read overlap with blocks that compute, so the rows kernel in
+// front pays late: at head size 128 (all rows in tiles / shared) 4 chunks among 40 170 / 196 us
+// (longest / mean 13), 1 among 65 172 / 186 us (52), 1 among 200 298 / 279 us (156); at 64,
+// where a tile's step takes as long for half the bytes, 143 / 147 us (13), 150 / 120 us (20),
+// 236 / 179 us (156).
+bool is_mixed(const attn::paged::PagedParams& p, int max_q_len, int D) {
+    return p.group <= 32 && (long long)max_q_len * p.n_seqs >= (D == 64 ? 16ll : 96ll) * p.total_q;
 }
 
 template <bool kF16, int kD>
@@ -236,7 +240,7 @@ attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, voi
     if constexpr (kD != 256) {
         if (takes_tiles(rows, kD, p.page_size)) {
             attn::paged::PagedParams half = p;
-            if (is_mixed(p, max_q_len)) {
+            if (is_mixed(p, max_q_len, kD)) {
                 half.split_rows = 8 * row_blocks_for(p.group, kD);
                 half.take_short = 1;
                 const attn_status_t st = launch_rows_for<kF16, kD>(half, p.group, workspace, sms, stream);

@@ -177,6 +177,16 @@ def test_fwd_many_sequences(n, kind):
         check(b, *run_fwd(b))
 
 
+@pytest.mark.parametrize("D,group", [(64, 4), (128, 3)])
+def test_fwd_one_chunk_among_single_tokens(D, group):
+    """Batches whose single tokens and chunks are different kernels' (many of the former)."""
+    lens = [(1 + 7 * i, 1) for i in range(150)]
+    lens[40], lens[90], lens[91] = (700, 300), (2, 2), (40, 0)
+    b = Batch(lens, 2 * group, 2, D, 16, pad_rows=2, seed=D)
+    for max_q in (300, 10 ** 6, 60):
+        check(b, *run_fwd(b, max_q_len=max_q), untouched=9.0)
+
+
 def test_fwd_one_long_sequence_among_many():
     """Shares that cut one unit many times and take others whole."""
     lens = [(30000, 1)] + [(rng, 1) for rng in range(1, 200)]
