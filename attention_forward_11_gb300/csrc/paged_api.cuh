@@ -53,6 +53,8 @@ bool opt_in_smem_rows() {
 template <bool kF16, int kD>
 bool opt_in_smem_rows_all() {
     if constexpr (kD == 256) return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>();
+    else if constexpr (kD == 128)
+        return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() && opt_in_smem_rows<kF16, kD, 3>();
     else return opt_in_smem_rows<kF16, kD, 1>() && opt_in_smem_rows<kF16, kD, 2>() &&
                 opt_in_smem_rows<kF16, kD, 3>() && opt_in_smem_rows<kF16, kD, 4>();
 }
@@ -103,9 +105,12 @@ unsigned long long next_tag() {
     return tag != 0 ? tag : 1;
 }
 
-// 8-row blocks of the rows kernel for sequences of at most `rows` (token, head) rows a
-// key/value head.  At head size 256 four blocks' sums do not fit the registers.
-int row_blocks_for(long long rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : rows <= 24 ? 3 : 4; }
+// Rows that the rows kernel computes together, in blocks of 8: as many as the registers hold
+// (at head size 128 a fourth block spills: 32 rows 109 us, 24 rows 62 us, on the same cache).
+int max_row_blocks(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+int row_blocks_for(long long rows, int D) {
+    return static_cast<int>(std::min<long long>((rows + 7) / 8, max_row_blocks(D)));
+}
 
 // Launched so that its blocks are in place while the kernel before it in the stream still
 // runs (if that one allows it); they wait for its end before they read or write anything.
@@ -141,10 +146,13 @@ attn_status_t launch_rows(const attn::paged::PagedParams& p, void* workspace, in
     return launch_behind(paged_rows_kernel<kF16, kD, kNB>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
 }
 
-// Does a call take the tcgen05 kernel?  From more than 32 rows a key/value head on (what
-// the rows kernel computes together), where pages can be gathered in boxes of 16 rows or
-// more and the head size has a kernel.
-bool takes_tiles(long long rows, int D, int page_size) { return rows > 32 && D <= 128 && page_size % 16 == 0; }
+// Does a call take the tcgen05 kernel?  From more rows a key/value head on than the rows kernel
+// computes together (16 sequences of 2000 to 6000 keys, rows / tiles kernel: 24 rows 62 / 63 us
+// at head size 128, 32 rows 41 / 49 us at 64; 8 rows 45 / 61 and 29 / 48), where pages can be
+// gathered in boxes of 16 rows or more and the head size has a kernel.
+bool takes_tiles(long long rows, int D, int page_size) {
+    return rows > 8 * max_row_blocks(D) && D <= 128 && page_size % 16 == 0;
+}
 
 size_t paged_workspace_bytes(int sms, long long rows, int D, int page_size) {
     return attn::paged::ws_bytes(sms, takes_tiles(rows, D, page_size) ? attn::kTiles * attn::kBM : 8 * row_blocks_for(rows, D), D);
@@ -215,10 +223,10 @@ attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows,
                               cudaStream_t stream) {
     const int nb = row_blocks_for(rows, kD);
     if (nb == 1) return launch_rows<kF16, kD, 1>(p, workspace, sms, stream);
-    if constexpr (kD != 256) {
+    if constexpr (kD != 256)
         if (nb == 3) return launch_rows<kF16, kD, 3>(p, workspace, sms, stream);
+    if constexpr (kD == 64)
         if (nb == 4) return launch_rows<kF16, kD, 4>(p, workspace, sms, stream);
-    }
     return launch_rows<kF16, kD, 2>(p, workspace, sms, stream);
 }
 
@@ -231,7 +239,7 @@ attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows,
 // where a tile's step takes as long for half the bytes, 143 / 147 us (13), 150 / 120 us (20),
 // 236 / 179 us (156).
 bool is_mixed(const attn::paged::PagedParams& p, int max_q_len, int D) {
-    return p.group <= 32 && (long long)max_q_len * p.n_seqs >= (D == 64 ? 16ll : 96ll) * p.total_q;
+    return p.group <= 8 * max_row_blocks(D) && (long long)max_q_len * p.n_seqs >= (D == 64 ? 16ll : 96ll) * p.total_q;
 }
 
 template <bool kF16, int kD>
