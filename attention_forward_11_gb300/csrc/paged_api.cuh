@@ -159,7 +159,8 @@ size_t paged_workspace_bytes(int sms, long long rows, int D, int page_size) {
 }
 
 template <bool kF16, int kD>
-attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, int sms, cudaStream_t stream) {
+attn_status_t launch_tiles(const attn::paged::PagedParams& p, long long rows, void* workspace, int sms,
+                           cudaStream_t stream) {
     using namespace attn::paged;
     using T = TilesGeo<kD>;
     EncodeTiledFn fn = encoder();
@@ -213,8 +214,11 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, void* workspace, i
     const attn_status_t st =
         launch_behind(kernel, dim3(sms), attn::kThreads, T::kSmemBytes, stream, tm[0], tm[1], tm[2], p, sp, tp);
     if (st != ATTN_OK) return st;
-    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>, dim3(sms, kCombineSplit<kD, T::kRows>),
-                         kCombineThreads, 0, stream, p, sp);
+    // blocks for the rows that units are likely to have: most find nothing to join
+    const int at_once = kCombineThreads / (kD / 4);
+    const int parts = static_cast<int>((std::min<long long>(rows, T::kRows) + at_once - 1) / at_once);
+    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>, dim3(sms, parts), kCombineThreads, 0,
+                         stream, p, sp);
 }
 
 // The rows kernel's variant for sequences of at most `rows` rows.
@@ -255,7 +259,7 @@ attn_status_t launch_paged(const attn::paged::PagedParams& p, int max_q_len, voi
                 if (st != ATTN_OK) return st;
                 half.take_short = 0;
             }
-            return launch_tiles<kF16, kD>(half, workspace, sms, stream);
+            return launch_tiles<kF16, kD>(half, rows, workspace, sms, stream);
         }
     }
     return launch_rows_for<kF16, kD>(p, rows, workspace, sms, stream);

@@ -399,15 +399,13 @@ __device__ __forceinline__ bool count_piece(unsigned long long* word, int n) {
 }
 
 // Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, the
-// sums in the order of the pieces.  Grid (G, kCombineSplit): block (c, y) has a part of the
+// sums in the order of the pieces.  Grid (G, parts of a unit's rows): block (c, y) has a part of the
 // rows of the unit that block c of the first kernel starts, kD / 4 threads a row with four
 // columns each.  Most units have two or three pieces, so what the kernel costs is its
 // instructions a row and how many loads wait on one another: those of the first kFly pieces
-// are in flight before M is known, and a thread has one row (with four rows a thread and an
-// eighth of the blocks a chunk of 64 tokens on 16000 took 48 instead of 38 us).
+// are in flight before M is known, and a thread has one row where units have so many (with
+// four rows a thread a chunk of 64 tokens on 16000 took 48 instead of 38 us).
 constexpr int kCombineThreads = 256;
-template <int kD, int kRows>
-constexpr int kCombineSplit = kRows / (kCombineThreads / (kD / 4));
 
 template <bool kF16, int kD, int kRows, int kTokenTiles>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __grid_constant__ PagedParams p,
@@ -421,53 +419,56 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
     const PieceHeader h = sp.ws.header[c];
     if (h.n == 0) return;
     const int col = threadIdx.x % kLanes * 4;
-    const int r = blockIdx.y * (kCombineThreads / kLanes) + threadIdx.x / kLanes;  // row of the unit
     const Seq x = seq_of(p, h.seq);
-    const int tile_tokens = sp.map.tokens / kTokenTiles, tile = r / kTileRows;
-    const Row w = row_of(p, sp.map, x, h.head_unit, h.row_unit * sp.map.tokens + tile * tile_tokens, tile_tokens,
-                         r % kTileRows);
-    if (!w.there) return;
-    // row of the workspace that holds piece i
-    auto ws_row = [&](int i) { return (size_t)piece_slot(c, i) * kRows + r; };
-    float2 ml[kFly];
-    float4 v[kFly];
-    auto load = [&](int i0) {
+    const int tile_tokens = sp.map.tokens / kTokenTiles;
+    constexpr int kAtOnce = kCombineThreads / kLanes;  // rows of a block
+    for (int r = blockIdx.y * kAtOnce + threadIdx.x / kLanes; r < kRows; r += gridDim.y * kAtOnce) {  // row of the unit
+        const int tile = r / kTileRows;
+        const Row w = row_of(p, sp.map, x, h.head_unit, h.row_unit * sp.map.tokens + tile * tile_tokens, tile_tokens,
+                             r % kTileRows);
+        if (!w.there) continue;
+        // row of the workspace that holds piece i
+        auto ws_row = [&](int i) { return (size_t)piece_slot(c, i) * kRows + r; };
+        float2 ml[kFly];
+        float4 v[kFly];
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-            ml[j] = make_float2(-INFINITY, 0.f);
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + j < h.n) {
-                ml[j] = sp.ws.ml[ws_row(i0 + j)];
-                v[j] = *reinterpret_cast<const float4*>(sp.ws.o + ws_row(i0 + j) * kD + col);
+            for (int j = 0; j < kFly; ++j) {
+                ml[j] = make_float2(-INFINITY, 0.f);
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + j < h.n) {
+                    ml[j] = sp.ws.ml[ws_row(i0 + j)];
+                    v[j] = *reinterpret_cast<const float4*>(sp.ws.o + ws_row(i0 + j) * kD + col);
+                }
             }
-        }
-    };
-    load(0);
-    float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    for (int i = kFly; i < h.n; ++i) M = fmaxf(M, sp.ws.ml[ws_row(i)].x);
-    const float use = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0;;) {
+        };
+        load(0);
+        float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+        for (int i = kFly; i < h.n; ++i) M = fmaxf(M, sp.ws.ml[ws_row(i)].x);
+        const float use = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0;;) {
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-            const float f = ex2_approx(ml[j].x - use);
-            L += ml[j].y * f;
-            acc.x += v[j].x * f;
-            acc.y += v[j].y * f;
-            acc.z += v[j].z * f;
-            acc.w += v[j].w * f;
+            for (int j = 0; j < kFly; ++j) {
+                const float f = ex2_approx(ml[j].x - use);
+                L += ml[j].y * f;
+                acc.x += v[j].x * f;
+                acc.y += v[j].y * f;
+                acc.z += v[j].z * f;
+                acc.w += v[j].w * f;
+            }
+            i0 += kFly;
+            if (i0 >= h.n) break;
+            load(i0);
         }
-        i0 += kFly;
-        if (i0 >= h.n) break;
-        load(i0);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const size_t tok = (size_t)x.q0 + w.token;
+        *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
+            make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
+        if (col == 0 && p.lse != nullptr)
+            p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const size_t tok = (size_t)x.q0 + w.token;
-    *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
-        make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
-    if (col == 0 && p.lse != nullptr)
-        p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace paged
