@@ -504,3 +504,32 @@ def test_two_streams_at_once():
         for o, lse in outs[i]:
             assert torch.equal(o, outs[i][0][0]) and torch.equal(lse, outs[i][0][1])
         check(b, *outs[i][0])
+
+
+@pytest.mark.parametrize("kind", ["none", "zero", "stream", "handle"])
+def test_streams_in_every_form(kind):
+    """A stream as torch's object, as a handle, as the default stream's handle 0, or none; the
+    calls allocate their outputs themselves, and another stream's allocations in between must
+    not disturb them."""
+    side = torch.cuda.Stream()
+    stream = {"none": None, "zero": 0, "stream": side, "handle": side.cuda_stream}[kind]
+    b = Batch([(9000, 1), (40, 1)], 8, 1, 64, 16, seed=40)
+    a = b.on_gpu()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        o, lse = fa.attn_paged_fwd(**a, max_q_len=1, stream=stream)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]  # on the current stream
+        del junk
+    one = torch.ones(2, dtype=I32, device="cuda")
+    torch.cuda.synchronize()
+    cu, kv, slots, counts = fa.attn_paged_tables(a["kv_lens"], one, torch.arange(8, dtype=I32, device="cuda") + 9000,
+                                                 a["block_table"], 16, 4, stream=stream)
+    k = torch.randn(4, 1, 64, device="cuda").to(BF)
+    torch.cuda.synchronize()
+    fa.attn_paged_append(k, k, slots, b.k_cache, b.v_cache, stream=stream)
+    torch.cuda.synchronize()
+    ok()
+    check(b, o, lse)
+    assert cu.tolist() == [0, 1, 2] and kv.tolist() == [9001, 41] and counts.tolist()[0] == 2
+    col = 40 // 16
+    assert slots.tolist()[1] == int(a["block_table"][1, col]) * 16 + 8 and slots.tolist()[2:] == [-1, -1]
