@@ -99,9 +99,10 @@ struct RowsGeo {
     static constexpr int kSmemBytes = kRing + kMerge + kStats;
     static_assert(kSmemBytes <= 231000, "ring, merge buffer and static shared memory exceed 227 KB");
     static_assert(kMerge >= kThreads / (kD / 4) * (kD + 4) * 4, "joined rows do not fit the merge buffer");
-    // a piece is worth its merge from two tiles on; cutting a unit costs its end some 4 us,
-    // which is the time of eight tiles when few blocks read
-    static constexpr int kMinPiece = 2, kMinShare = 8;
+    // a piece is worth its merge from two tiles on, and so is a share (one sequence of 1000 or
+    // 5000 keys, 8 heads: 9.7 and 10.9 us; shares of at least 4 tiles 11.1 and 11.4, 8 tiles
+    // 11.0 and 15.3); units up to 8 tiles longer than a share stay whole
+    static constexpr int kMinPiece = 2, kMinShare = 2, kCutTiles = 8;
     using ShareT = Share<kTileKeys, kMinPiece, kMinShare>;
     using CursorT = Cursor<ShareT, kTileKeys>;
 };
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(RowsGeo<kD, kNB>::kThreads, 1)
     wait_for_primary();
 
     typename G::ShareT sh;
-    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare, false>(p, sp, s_part, &s_start, sh);
+    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare, G::kCutTiles, false>(p, sp, s_part, &s_start, sh);
     if (!some) return;
     typename G::CursorT cur;
     cur.first(p, sp, sh, s_start);

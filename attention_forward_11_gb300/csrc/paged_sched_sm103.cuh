@@ -171,9 +171,7 @@ __device__ __forceinline__ long long block_sum(long long v, long long* part) {
 
 // The share of block blockIdx.x and the sequence it starts in (block-wide; `part`, three
 // values a warp, and `found` are shared scratch).  Returns false for a block without work.
-constexpr int kCutTiles = 8;  // key tiles that take as long as a cut unit's end
-
-template <int kThreads, class ShareT, int kTile, int kMinShare, bool kAlign>
+template <int kThreads, class ShareT, int kTile, int kMinShare, int kCutTiles, bool kAlign>
 __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedParams& sp, long long* part, StartPos* found,
                                            ShareT& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
