@@ -9,16 +9,20 @@
 // are the long side of the warp-level products m16n8k16, rows the short one:
 //   S^T [16 keys x 8 rows]  = K Q^T     A = K from shared memory, B = Q in registers
 //   O^T [16 of D x 8 rows] += V^T P^T   A = V from shared memory transposed, B = P^T
-// A warp owns 16 keys of every tile and keeps its own running maximum, sum and O^T
-// (online softmax in log2 units, fp32), so warps meet only at the end of a unit, where
-// their (m, l, O) are merged in a fixed order.  P is rounded to the operands' type for
-// its product, as in the dense forward.
+// A warp owns a slice of every tile, 16 keys (32 at head size 64), and keeps its own running
+// maximum, sum and O^T (online softmax in log2 units, fp32), so warps meet only at the end
+// of a unit, where their (m, l, O) are merged in a fixed order.  P is rounded to the
+// operands' type for its product, as in the dense forward.
 //
 // One block a SM takes an equal share of the batch (paged_sched_sm103.cuh); of the blocks
 // that have a piece of one unit, the last to finish joins them.  Each warp
 // fills a ring of its own with cp.async, two slices ahead of the one it computes and across
 // the ends of units, with no barrier between warps: 16-byte copies follow any page size and
-// any strides, and a slice's page numbers are read one slice earlier still.
+// any strides, and a slice's page numbers are read one slice earlier still.  192 KB of
+// slices keep HBM busy: 256 sequences of 100 to 4000 keys take 320 us (6.6 TB/s of cache),
+// 48 of 300 to 8000 113 us (6.0 TB/s).  Short calls are a block's start (4 us to the first
+// copies) and end (merge and join, 5 us): 8 sequences of 32768 keys 29.7 us (19.8 at HBM's
+// rate), one of 1000 keys 9.6 us.
 #pragma once
 #include <cmath>
 #include <cstdint>

@@ -256,8 +256,8 @@ attn_status_t attn_paged_tables(const int* ctx_lens, const int* new_lens, int n_
  * k_cache, v_cache, n_pages .. head_stride  the cache, as above; D 64, 128 or 256
  *           (other head sizes: ATTN_ERR_UNSUPPORTED).  It overlaps no other argument.
  *
- * The rows are copied as they are (bf16 and fp16 alike).  Asynchronous on `stream`, one
- * kernel; on any error return nothing was launched.
+ * The rows are copied as they are (bf16 and fp16 alike).  Every size is at least 1.
+ * Asynchronous on `stream`, one kernel; on any error return nothing was launched.
  */
 attn_status_t attn_paged_append(const void* k, const void* v, const long long* slot_map, void* k_cache,
                                 void* v_cache, int n_tokens, int Hkv, int D, int n_pages, int page_size,
@@ -293,7 +293,7 @@ attn_status_t attn_paged_append(const void* k, const void* v, const long long* s
  *              the same total_q .. page_size).  Scratch: its contents are undefined before
  *              and after the call, and calls that overlap in time on the GPU must not
  *              share one.
- * total_q * Hq is at most 2^31 - 1.
+ * Every size is at least 1; total_q * Hq is at most 2^31 - 1.
  *
  * Arithmetic as attn_fwd: operands and P in the element type, products and softmax
  * statistics in fp32, O rounded to nearest even once.  Results do not depend on timing:
