@@ -351,28 +351,30 @@ def _check_ints(name, t, dtype, n):
         _bad(name, f"a contiguous {dtype} tensor of {n}")
 
 
-def _table_stride(table, n_seqs, i32):
-    if table.dtype is not i32 or table.dim() != 2 or table.shape[0] != n_seqs or table.stride(1) != 1:
+def _table_shape(table, n_seqs, i32):
+    """(columns, row stride) of a block table."""
+    shape, stride = table.shape, table.stride()
+    if table.dtype is not i32 or len(shape) != 2 or shape[0] != n_seqs or stride[1] != 1:
         _bad("block_table", "int32 [n_seqs, max_pages] with contiguous rows")
-    return table.stride(0) if n_seqs > 1 else table.shape[1]
+    return shape[1], stride[0] if n_seqs > 1 else shape[1]
 
 
-def _check_cache(k_cache, v_cache, what, dtype, types):
-    if dtype not in types or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+def _cache_shape(torch, k_cache, v_cache, what, dtype):
+    """(shape, strides) of both caches."""
+    if (dtype is not torch.bfloat16 and dtype is not torch.float16) or k_cache.dtype is not dtype or \
+            v_cache.dtype is not dtype:
         _bad(f"{what} and the cache", "bf16 or float16, all one type")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or \
-            k_cache.stride(3) != 1:
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != stride or stride[3] != 1:
         _bad("k_cache and v_cache", "[n_pages, page_size, Hkv, D] of one shape and strides, D contiguous")
+    return shape, stride
 
 
-def _row_stride(name, t, heads, D):
+def _row_stride(name, shape, stride, heads, D):
     """Row stride of [T, heads, D] with contiguous heads (a slice of a wider row is fine)."""
-    if t.dim() == 3:
-        T, h, d = t.shape
-        row, head, one = t.stride()
-        if h == heads and d == D and one == 1 and (head == D or heads == 1):
-            return row if T > 1 else heads * D
-    _bad(name, f"[T, {heads}, {D}] with contiguous heads")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or stride[2] != 1 or (stride[1] != D and heads > 1):
+        _bad(name, f"[T, {heads}, {D}] with contiguous heads")
+    return stride[0] if shape[0] > 1 else heads * D
 
 
 def attn_paged_tables_ptr(*args) -> int:
@@ -424,7 +426,7 @@ def _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, pa
         _check_ints("free_pages", free_pages, i32, n_free)
     if free_head is not None:
         _check_ints("free_head", free_head, i32, 1)
-    table_stride = _table_stride(block_table, n, i32)
+    max_pages, table_stride = _table_shape(block_table, n, i32)
     device = ctx_lens.device
     if cu_new is None:
         cu_new = torch.empty(n + 1, dtype=i32, device=device)
@@ -444,7 +446,7 @@ def _paged_tables(torch, handle, ctx_lens, new_lens, free_pages, block_table, pa
         _check_ints("counts", counts, i32, 4)
     st = attn_paged_tables_ptr(ctx_lens.data_ptr(), new_lens.data_ptr(), n, page_size, free_pages.data_ptr(), n_free,
                                0 if free_head is None else free_head.data_ptr(), block_table.data_ptr(),
-                               block_table.shape[1], table_stride, cu_new.data_ptr(), kv_lens.data_ptr(),
+                               max_pages, table_stride, cu_new.data_ptr(), kv_lens.data_ptr(),
                                slot_map.data_ptr(), max_tokens, counts.data_ptr(), handle)
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_tables")
@@ -457,15 +459,14 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
     ([n_pages, page_size, Hkv, D], any strides with D contiguous), in place."""
     torch = _torch or _load_torch()
     device = _on_one_gpu(k, v, slot_map, k_cache, v_cache)
-    _check_cache(k_cache, v_cache, "k, v", k.dtype, (torch.bfloat16, torch.float16))
-    n_pages, page_size, Hkv, D = k_cache.shape
-    T = k.shape[0]
-    if v.dtype is not k.dtype or v.shape[0] != T:
-        _bad("v", "of k's type, with as many rows")
+    dtype, shape = k.dtype, k.shape
+    (n_pages, page_size, Hkv, D), (ps, ts, hs, _) = _cache_shape(torch, k_cache, v_cache, "k, v", dtype)
+    T = shape[0]
+    if v.dtype is not dtype or v.shape != shape:
+        _bad("v", "of k's type and shape")
     _check_ints("slot_map", slot_map, torch.int64, T)
-    ps, ts, hs, _ = k_cache.stride()
     args = (k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, D, n_pages,
-            page_size, _row_stride("k", k, Hkv, D), _row_stride("v", v, Hkv, D), ps, ts, hs)
+            page_size, _row_stride("k", shape, k.stride(), Hkv, D), _row_stride("v", shape, v.stride(), Hkv, D), ps, ts, hs)
     if stream is None and torch._C._cuda_getDevice() == device:
         st = attn_paged_append_ptr(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
@@ -509,24 +510,24 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: i
 
 def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len, causal, scale, o, lse, workspace,
                want_lse):
-    dtype, i32 = q.dtype, torch.int32
-    _check_cache(k_cache, v_cache, "q", dtype, (torch.bfloat16, torch.float16))
-    n_pages, page_size, Hkv, D = k_cache.shape
+    dtype, i32, shape = q.dtype, torch.int32, q.shape
+    (n_pages, page_size, Hkv, D), (ps, ts, hs, _) = _cache_shape(torch, k_cache, v_cache, "q", dtype)
     n = kv_lens.numel()
-    _check_ints("kv_lens", kv_lens, i32, n)
-    _check_ints("cu_q", cu_q, i32, n + 1)
-    if q.dim() != 3:
+    if not (kv_lens.dtype is i32 and cu_q.dtype is i32 and kv_lens.dim() == 1 and cu_q.dim() == 1 and
+            cu_q.numel() == n + 1 and kv_lens.is_contiguous() and cu_q.is_contiguous()):
+        _check_ints("kv_lens", kv_lens, i32, n)
+        _check_ints("cu_q", cu_q, i32, n + 1)
+    if len(shape) != 3:
         _bad("q", "[T, Hq, D]")
-    T, Hq, _ = q.shape
-    q_stride = _row_stride("q", q, Hq, D)
-    table_stride = _table_stride(block_table, n, i32)
-    ps, ts, hs, _ = k_cache.stride()
+    T, Hq, _ = shape
+    q_stride = _row_stride("q", shape, q.stride(), Hq, D)
+    max_pages, table_stride = _table_shape(block_table, n, i32)
     if o is None:
         o = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
-    elif o.dtype is not dtype or tuple(o.shape) != (T, Hq, D) or not o.is_contiguous():
+    elif o.dtype is not dtype or o.shape != shape or not o.is_contiguous():
         _bad("o", "a contiguous [T, Hq, D] tensor of q's type")
     if lse is not None:
-        if lse.dtype is not torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+        if lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
             _bad("lse", "a contiguous float32 [Hq, T] tensor")
     elif want_lse:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
@@ -537,7 +538,7 @@ def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, m
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     st = attn_paged_fwd_ptr(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
                             0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                            kv_lens.data_ptr(), n, T, max_q_len, Hq, Hkv, D, n_pages, page_size, block_table.shape[1],
+                            kv_lens.data_ptr(), n, T, max_q_len, Hq, Hkv, D, n_pages, page_size, max_pages,
                             q_stride, table_stride, ps, ts, hs, causal, D ** -0.5 if scale is None else scale,
                             ATTN_DTYPE_F16 if dtype is torch.float16 else ATTN_DTYPE_BF16, workspace.data_ptr(),
                             workspace.nbytes, handle)
