@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(kTableThreads) paged_tables_kernel(const Table
     __shared__ long long s_tok[kTableThreads], s_page[kTableThreads];  // tokens / new pages before the sequence
     __shared__ int s_ctx[kTableThreads], s_have[kTableThreads];
     __shared__ long long s_part[2][32];
-    launch_dependents();
     wait_for_primary();
     const int tid = threadIdx.x, G = gridDim.x, c = blockIdx.x;
     const long long head = p.free_head != nullptr ? max(*p.free_head, 0) : 0;
@@ -133,6 +132,7 @@ __global__ void __launch_bounds__(kTableThreads) paged_tables_kernel(const Table
         page = page_end;
         __syncthreads();
     }
+    launch_dependents();  // late: with it in front the next kernel's blocks cost 1024 sequences 2 us
     for (long long t = max((long long)t0, tok) + tid; t < t1; t += kTableThreads) p.slot_map[t] = -1;
     if (c == 0) {
         long long x = too_long, unused = 0;

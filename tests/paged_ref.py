@@ -25,7 +25,7 @@ class Batch:
     """A ragged batch over a paged cache: lens = [(cached + new keys, new rows), ...]."""
 
     def __init__(self, lens, Hq, Hkv, D, page, dtype=torch.bfloat16, causal=1, layout="tokens", extra_cols=2,
-                 pad_rows=0, seed=0, stale=float("nan"), q_sigma=1.0, first_page=0, device="cuda"):
+                 pad_rows=0, seed=0, stale=float("nan"), q_sigma=1.0, first_page=0, device="cuda", shift=0.0):
         self.lens, self.Hq, self.Hkv, self.D, self.page = lens, Hq, Hkv, D, page
         self.dtype, self.causal, self.device = dtype, causal, device
         rng = random.Random(seed)
@@ -45,6 +45,8 @@ class Batch:
             at += counts[s]
             table[s, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
             dk = torch.randn(kv, Hkv, D, generator=g).to(dtype)
+            if shift:  # with q[..., 0] = 16 below: every logit is moved by about `shift`
+                dk[..., 0] = shift * math.sqrt(D) / 16
             dv = torch.randn(kv, Hkv, D, generator=g).to(dtype)
             self.dense.append((dk, dv))
             for j, x in enumerate(pages):
@@ -55,6 +57,8 @@ class Batch:
         self.cu = np.cumsum([0] + [n for _, n in lens]).tolist()
         self.T = self.cu[-1] + pad_rows
         self.q = (q_sigma * torch.randn(max(self.T, 1), Hq, D, generator=g)).to(dtype)
+        if shift:
+            self.q[..., 0] = 16
         self.scale = 1 / math.sqrt(D)
         self.k_cache, self.v_cache = self._place(k, v, layout, first_page)
 

@@ -339,10 +339,11 @@ def test_fwd_long_caches(lens, Hq, Hkv, D):
     check(b, *run_fwd(b))
 
 
-def test_fwd_wide_rows_of_a_fused_projection():
-    b = Batch(MIXED, 8, 2, 64, 16, seed=6)
+@pytest.mark.parametrize("D", [64, 128])
+def test_fwd_wide_rows_of_a_fused_projection(D):
+    b = Batch(MIXED, 8, 2, D, 16, seed=6)
     a = b.on_gpu()
-    x = torch.randn(b.T, 12, 64, device="cuda").to(BF)
+    x = torch.randn(b.T, 12, D, device="cuda").to(BF)
     x[:, :8] = a["q"]
     a["q"] = x[:, :8]
     wide = torch.full((len(b.lens), b.table.shape[1] + 5), 2 ** 30, dtype=I32, device="cuda")
@@ -351,6 +352,34 @@ def test_fwd_wide_rows_of_a_fused_projection():
     for max_q in (1, 1000):
         check(b, *fa.attn_paged_fwd(**a, max_q_len=max_q, causal=1))
         ok()
+
+
+@pytest.mark.parametrize("shift", [-60.0, -17.3, 40.0])
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, HF), (128, BF), (256, HF)])
+@pytest.mark.parametrize("lens", [DECODE, MIXED], ids=["decode", "mixed"])
+def test_fwd_logits_far_from_zero(lens, D, dtype, shift):
+    """Weights are relative to the row's own maximum, however far below zero that is: fp16
+    weights relative to anything higher would vanish."""
+    b = Batch(lens, 4, 2, D, 16, dtype, seed=15, shift=shift)
+    check(b, *run_fwd(b))
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.7])
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, HF), (256, HF)])
+def test_fwd_arguments_left_out_and_other_scales(D, dtype, scale):
+    b = Batch(MIXED, 4, 2, D, 32, dtype, seed=14)
+    a = b.on_gpu()
+    b.scale = scale
+    o, lse = fa.attn_paged_fwd(**a, scale=scale)                  # max_q_len left out
+    ok()
+    check(b, o, lse)
+    o2, none = fa.attn_paged_fwd(**a, scale=scale, want_lse=False)
+    ok()
+    assert none is None and torch.equal(o, o2)
+    big = torch.empty(64 << 20, dtype=torch.float32, device="cuda")  # more workspace than needed, another type
+    o3, lse3 = fa.attn_paged_fwd(**a, scale=scale, workspace=big)
+    ok()
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
 @pytest.mark.parametrize("D", [64, 128])
