@@ -685,12 +685,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int q = 0; q < 8; ++q)
                     mx[q] = fmax3(__uint_as_float(s[q]), __uint_as_float(s[8 + q]), __uint_as_float(s[16 + q]));
 #pragma unroll
-                for (int base = 24; base < kBN; base += 16)
+                for (int base = 24; base + 16 <= kBN; base += 16)
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         mx[q] = fmax3(mx[q], __uint_as_float(s[base + q]), __uint_as_float(s[base + 8 + q]));
-                const float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                         fmaxf(mx[6], mx[7]));
+                // the last eight logits join the chains' tree
+                auto last = [&](int q) { return __uint_as_float(s[kBN - 8 + q]); };
+                const float tmax = fmaxf(fmax3(fmax3(mx[0], mx[1], last(0)), fmax3(mx[2], mx[3], last(1)),
+                                               fmax3(mx[4], mx[5], last(2))),
+                                         fmax3(fmax3(mx[6], mx[7], last(3)), fmax3(last(4), last(5), last(6)), last(7)));
                 const float m_tile = tmax * sl2;
 
                 // raise the running max only when the tile max exceeds it by more than 2^15
