@@ -495,7 +495,7 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: i
     sequences' rows of q; kv_lens: int32 [n_seqs], keys in the cache, the new ones
     included.  max_q_len: the longest sequence's rows, which chooses the kernel (None: T).
     causal: 1 (aligned at the end) or 0.  Returns (o [T, Hq, D], lse fp32 [Hq, T] or None);
-    rows of no sequence are left as they were.  `workspace`: a CUDA byte tensor of at least
+    rows of no sequence are left as they were.  `workspace`: a contiguous CUDA tensor of at least
     attn_paged_fwd_workspace_size(...) bytes; it and the outputs are allocated here if None.
     """
     torch = _torch or _load_torch()
@@ -536,6 +536,8 @@ def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, m
     if workspace is None:
         size = attn_paged_fwd_workspace_size(T, max_q_len, Hq, Hkv, D, page_size)
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        _bad("workspace", "contiguous")
     st = attn_paged_fwd_ptr(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
                             0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
                             kv_lens.data_ptr(), n, T, max_q_len, Hq, Hkv, D, n_pages, page_size, max_pages,

@@ -125,3 +125,29 @@ def test_plain_tables_by_hand():
     assert table == [[5, 8], [-1, -1], [6, 9]]
     assert cu == [0, 3, 3, 4] and kv == [6, 0, 5] and counts == [4, 3, 0, 0]
     assert slots == [5 * 4 + 3, 8 * 4, 8 * 4 + 1, 9 * 4, -1, -1]
+
+
+def recorded(monkeypatch, name):
+    """Argument tuples that the binding hands to a C entry point, which is not called."""
+    calls = []
+    monkeypatch.setattr(fa._binding, name, lambda *args: calls.append(args) or fa.ATTN_OK)
+    return calls
+
+
+@pytest.mark.parametrize("kind", ["strided", "expanded", "reversed axes", "column"])
+def test_a_workspace_with_gaps_is_refused(kind, monkeypatch):
+    """The kernels write `nbytes` from the first byte on: a view that has fewer of its own there would
+    have its neighbours' bytes, or bytes past its storage, written."""
+    calls = recorded(monkeypatch, "attn_paged_fwd_ptr")
+    u8 = torch.uint8
+    ws = {"strided": torch.zeros(8192, dtype=u8)[::2], "expanded": torch.zeros(1, dtype=u8).expand(1 << 20),
+          "reversed axes": torch.zeros(64, 128, dtype=u8).t(), "column": torch.zeros(4096, 2, dtype=u8)[:, 0]}[kind]
+    b = Batch([(20, 3)], 4, 2, 64, 16, device="cpu")
+    a = b.on_gpu()
+    args = [torch, 0, *a.values(), 3, 1, None, None, None]
+    with pytest.raises(fa.AttnError, match="workspace") as e:
+        fa._binding._paged_fwd(*args, ws, True)
+    assert e.value.status == fa.ATTN_ERR_INVALID_ARG and not calls
+    whole = torch.zeros(64, 128, dtype=torch.float32)
+    fa._binding._paged_fwd(*args, whole, True)
+    assert len(calls) == 1 and calls[0][-3:] == (whole.data_ptr(), 64 * 128 * 4, 0)
