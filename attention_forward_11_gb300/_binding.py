@@ -125,6 +125,12 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _check_workspace(workspace, q):
+    # the kernels write its bytes one after another, from the first on
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise AttnError(ATTN_ERR_INVALID_ARG, "workspace must be a contiguous tensor on q's device")
+
+
 def attn_fwd_ptr(q: int, k: int, v: int, o: int, lse: int, B: int, Sq: int, Skv: int, Hq: int,
                  Hkv: int, D: int, causal: int, scale: float, stream: int) -> int:
     """Raw-pointer call of the C entry point; returns the attn_status_t value."""
@@ -201,9 +207,10 @@ def attn_fwd_splitkv_ptr(q: int, k: int, v: int, o: int, lse: int, B: int, Sq: i
 
 def attn_fwd_splitkv(q, k, v, o=None, lse=None, causal: int = 0, scale: float | None = None,
                      workspace=None, stream=None, want_lse: bool = True):
-    """attn_fwd with KV split across SMs.  `workspace`: a CUDA byte tensor of at
+    """attn_fwd with KV split across SMs.  `workspace`: a contiguous CUDA byte tensor of at
     least attn_fwd_splitkv_workspace_size(...) bytes, allocated here if None."""
     import torch
+    _check_workspace(workspace, q)
     B, Sq, Hq, D = q.shape
     Skv, Hkv = k.shape[1], k.shape[2]
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -258,8 +265,10 @@ def attn_bwd(q, k, v, o, lse, do, causal: int = 0, scale: float | None = None, d
              dv=None, workspace=None, stream=None):
     """dq, dk, dv of sum(do * o) for o = attn_fwd(q, k, v, causal, scale); o and lse
     are that forward's outputs.  bf16 or float16 CUDA tensors (all the same type),
-    lse fp32 [B, Hq, Sq].  Outputs and the workspace are allocated here if None."""
+    lse fp32 [B, Hq, Sq].  Outputs and the workspace (contiguous bytes) are allocated here if
+    None."""
     import torch
+    _check_workspace(workspace, q)
     B, Sq, Hq, D = q.shape
     Skv, Hkv = k.shape[1], k.shape[2]
     if q.dtype not in (torch.bfloat16, torch.float16):

@@ -318,3 +318,19 @@ def test_unit_table_rejects_bad_arguments():
                                         ctypes.byref(n)) == fa.ATTN_ERR_INVALID_ARG   # Hq % Hkv
     assert lib.attn_debug_unit_schedule(4, 4096, 4096, 16, 16, 96, 1, 152, beg, buf, 4096,
                                         ctypes.byref(n)) == fa.ATTN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", ["attn_fwd_splitkv", "attn_bwd"])
+@pytest.mark.parametrize("kind", ["strided", "expanded", "another device"])
+def test_binding_refuses_a_workspace_with_gaps_or_elsewhere(call, kind):
+    """Its bytes are written one after another by kernels on q's device."""
+    import torch
+    ws = {"strided": torch.zeros(8192, dtype=torch.uint8)[::2],
+          "expanded": torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+          "another device": torch.empty(1 << 20, dtype=torch.uint8, device="meta")}[kind]
+    x = torch.zeros(1, 128, 2, 64, dtype=torch.bfloat16)
+    lse = torch.zeros(1, 2, 128)
+    args = (x, x, x) if call == "attn_fwd_splitkv" else (x, x, x, x, lse, x)
+    with pytest.raises(fa.AttnError, match="workspace") as e:
+        getattr(fa, call)(*args, workspace=ws)
+    assert e.value.status == fa.ATTN_ERR_INVALID_ARG
