@@ -338,6 +338,8 @@ class _on:
         else:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", device))
+            elif stream.device.index != device:
+                _bad("stream", "a stream of the tensors' device")
             self.handle = stream.cuda_stream
             self.guards.append(torch.cuda.stream(stream))
 

@@ -151,3 +151,17 @@ def test_a_workspace_with_gaps_is_refused(kind, monkeypatch):
     whole = torch.zeros(64, 128, dtype=torch.float32)
     fa._binding._paged_fwd(*args, whole, True)
     assert len(calls) == 1 and calls[0][-3:] == (whole.data_ptr(), 64 * 128 * 4, 0)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """A launch goes to the stream's device, where the tensors' addresses mean nothing."""
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s))
+    mine = SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=5)
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=5)
+    assert fa._binding._on(0, mine).handle == 5
+    with pytest.raises(fa.AttnError, match="stream") as e:
+        fa._binding._on(0, other)
+    assert e.value.status == fa.ATTN_ERR_INVALID_ARG and entered == [mine]
