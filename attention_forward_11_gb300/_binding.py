@@ -376,7 +376,8 @@ def _cache_shape(torch, k_cache, v_cache, what, dtype):
             v_cache.dtype is not dtype:
         _bad(f"{what} and the cache", "bf16 or float16, all one type")
     shape, stride = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != stride or stride[3] != 1:
+    if len(shape) != 4 or v_cache.shape != shape or stride[3] != 1 or (v_cache.stride() != stride and any(
+            n > 1 and x != y for n, x, y in zip(shape, stride, v_cache.stride()))):  # an axis of one has no stride
         _bad("k_cache and v_cache", "[n_pages, page_size, Hkv, D] of one shape and strides, D contiguous")
     return shape, stride
 

@@ -165,3 +165,21 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     with pytest.raises(fa.AttnError, match="stream") as e:
         fa._binding._on(0, other)
     assert e.value.status == fa.ATTN_ERR_INVALID_ARG and entered == [mine]
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_caches_whose_strides_differ_on_an_axis_of_one(axis):
+    """Such a stride has no meaning, so K and V of unlike origin are still one layout."""
+    shape = [3, 16, 2, 64]
+    shape[axis] = 1
+    k = torch.zeros(shape, dtype=torch.bfloat16)
+    wide = list(k.stride())
+    wide[axis] += 8
+    v = k.as_strided(shape, wide)
+    got, strides = fa._binding._cache_shape(torch, k, v, "q", torch.bfloat16)
+    assert tuple(got) == tuple(shape) and strides == k.stride()
+    other = (axis + 1) % 3  # an axis that has more than one
+    room = torch.zeros(10 * k.numel(), dtype=torch.bfloat16)
+    wide = [2 * x if i == other else x for i, x in enumerate(k.stride())]
+    with pytest.raises(fa.AttnError, match="strides"):
+        fa._binding._cache_shape(torch, k, room.as_strided(shape, wide), "q", torch.bfloat16)
