@@ -243,7 +243,9 @@ attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows,
 // where a tile's step takes as long for half the bytes, 143 / 147 us (13), 150 / 120 us (20),
 // 236 / 179 us (156).
 bool is_mixed(const attn::paged::PagedParams& p, int max_q_len, int D) {
-    return p.group <= 8 * max_row_blocks(D) && (long long)max_q_len * p.n_seqs >= (D == 64 ? 16ll : 96ll) * p.total_q;
+    // of a batch padded with empty sequences no more have rows than there are rows beside the longest's
+    const long long n = max_q_len < p.total_q ? std::min(p.n_seqs, p.total_q - max_q_len + 1) : p.n_seqs;
+    return p.group <= 8 * max_row_blocks(D) && max_q_len * n >= (D == 64 ? 16ll : 96ll) * p.total_q;
 }
 
 template <bool kF16, int kD>

@@ -625,3 +625,23 @@ def test_fwd_empty_places_of_a_batch(name, lens, Hq, Hkv, D, n, step, times):
     if name != "mixed":  # there the empty places may choose other kernels
         assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     assert took[1] <= times * took[0], f"{took[0]:.1f} us, among {n} places {took[1]:.1f} us"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fwd_empty_places_are_no_single_tokens(D):
+    """A chunk and three tokens in 1024 places are no batch of many tokens: two kernels, the second
+    joining the first one's pieces, as without the empty places."""
+    lens = [(700, 512), (40, 1), (100, 1), (7, 1)]
+    b = Batch(lens, 8, 2, D, 16, seed=D)
+    a = padded(b.on_gpu(), [3, 200, 201, 1000], 1024)
+    before = fa.attn_kernel_launches()
+    o, lse = fa.attn_paged_fwd(**a, max_q_len=512)
+    ok()
+    assert fa.attn_kernel_launches() == before + 2
+    check(b, o, lse)
+    many = Batch([(700, 512)] + [(40, 1)] * 900, 2, 1, D, 16, seed=D)  # a batch of many tokens: three
+    before = fa.attn_kernel_launches()
+    o, lse = fa.attn_paged_fwd(**many.on_gpu(), max_q_len=512)
+    ok()
+    assert fa.attn_kernel_launches() == before + 3
+    check(many, o, lse)
