@@ -231,8 +231,12 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
             n_units *= sp.map.head_units;
             const long long c = blockIdx.x, G = gridDim.x;
             // Whole units where the longest is no longer than an equal share and what a cut
-            // costs at its end (kCutTiles), or, where units share K/V tiles in L2 (kAlign: they
-            // all start at key 0 and keep in step), than 1.35 shares.
+            // costs at its end (kCutTiles), or, where units share K/V tiles in L2 and need them
+            // as fast as L2 gives them (kAlign; whole units all start at key 0 and keep in step),
+            // than 1.35 shares.  576 to 416 tokens, 64/8 heads, on 32000 keys, longest / share 1.06,
+            // 1.19, 1.36, 1.46: whole / cut 341 / 435, 345 / 385, 333 / 350, 331 / 317 us at head
+            // size 128; on 8000 keys 101 / 110, 101 / 100, 99 / 90.  At 64, where a tile's softmax
+            // takes longer than its bytes, 294 / 286, 296 / 256, 296 / 226, 294 / 211: no kAlign.
             const long long share = quotient(total, G);
             longest += kUnitKeys;
             sh.whole = n_units <= G && (longest <= share + kCutTiles * kTile || (kAlign && longest * 100 <= share * 135));

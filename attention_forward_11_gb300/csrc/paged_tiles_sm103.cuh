@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_for_primary();
     typename T::ShareT sh;
     if (threadIdx.x == 0) sp.ws.header[blockIdx.x].n = 0;
-    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare, T::kCutTiles, true>(
+    if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare, T::kCutTiles, kD == 128>(
             p, sp, reinterpret_cast<long long*>(smem + T::kSmemPart), start, sh)) {
         if (warp == 0) tmem_dealloc(tmem_base, kTmemCols);
         return;

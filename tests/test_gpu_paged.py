@@ -645,3 +645,16 @@ def test_fwd_empty_places_are_no_single_tokens(D):
     ok()
     assert fa.attn_kernel_launches() == before + 3
     check(many, o, lse)
+
+
+def test_fwd_units_of_a_few_more_keys_than_a_share_are_cut():
+    """Head size 64: a chunk of 128 blocks of rows leaves no 24 of 152 SMs idle, which a chunk of 152
+    blocks takes whole (0.86 of its time; with whole units 1.0)."""
+    took = []
+    for n in (608, 512):
+        b = Batch([(32000 + n, n)], 64, 8, 64, 64, seed=n)
+        a = b.on_gpu()
+        ws = torch.empty(fa.attn_paged_fwd_workspace_size(n, n, 64, 8, 64, 64), dtype=torch.uint8, device="cuda")
+        took.append(device_us(lambda: fa.attn_paged_fwd(**a, max_q_len=n, workspace=ws)))
+        ok()
+    assert took[1] <= 0.94 * took[0], f"608 rows {took[0]:.0f} us, 512 rows {took[1]:.0f} us"
