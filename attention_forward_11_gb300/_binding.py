@@ -489,7 +489,7 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, stream=None) -> None:
 
 
 def attn_paged_fwd_workspace_size(total_q: int, max_q_len: int, Hq: int, Hkv: int, D: int, page_size: int) -> int:
-    """Workspace bytes attn_paged_fwd needs on the current device (0: none)."""
+    """Workspace bytes attn_paged_fwd needs on the current device."""
     n = ctypes.c_size_t(0)
     st = int(load_library().attn_paged_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, ctypes.byref(n)))
     if st != ATTN_OK:
@@ -505,7 +505,8 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_q, kv_lens, max_q_len: i
     fine); k_cache, v_cache: [n_pages, page_size, Hkv, D] of q's type, any strides with D
     contiguous; block_table: int32 [n_seqs, max_pages]; cu_q: int32 [n_seqs + 1], the
     sequences' rows of q; kv_lens: int32 [n_seqs], keys in the cache, the new ones
-    included.  max_q_len: the longest sequence's rows, which chooses the kernel (None: T).
+    included.  max_q_len: the longest sequence's rows, which chooses the kernel.  None takes T,
+    which is right but slow for a batch of single or drafted tokens: pass 1, or their number.
     causal: 1 (aligned at the end) or 0.  Returns (o [T, Hq, D], lse fp32 [Hq, T] or None);
     rows of no sequence are left as they were.  `workspace`: a contiguous CUDA tensor of at least
     attn_paged_fwd_workspace_size(...) bytes; it and the outputs are allocated here if None.

@@ -107,6 +107,10 @@ unsigned long long next_tag() {
 
 // Rows that the rows kernel computes together, in blocks of 8: as many as the registers hold
 // (at head size 128 a fourth block spills: 32 rows 109 us, 24 rows 62 us, on the same cache).
+// At 256 the second block spills too, 158 bytes, and still pays where the cache's bytes bound
+// the call: 16 rows on 16 x 2000 to 6000 keys 117 us, as twice 8 rows 137 us, on 2 x 20000 keys
+// 89 / 107 us.  Short and computing calls lose: on 1000 keys 23 / 14.5 us, 512 tokens on 8000
+// keys 1616 / 1476 us.
 int max_row_blocks(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 int row_blocks_for(long long rows, int D) {
     return static_cast<int>(std::min<long long>((rows + 7) / 8, max_row_blocks(D)));
@@ -238,10 +242,13 @@ attn_status_t launch_rows_for(const attn::paged::PagedParams& p, long long rows,
 // their own?  The lengths are on the device; on the host the longest sequence against the
 // mean tells.  A row tile with one token in it takes a key tile about as fast as the cache
 // can be read, and blocks that read overlap with blocks that compute, so the rows kernel in
-// front pays late: at head size 128 (all rows in tiles / shared) 4 chunks among 40 170 / 196 us
-// (longest / mean 13), 1 among 65 172 / 186 us (52), 1 among 200 298 / 279 us (156); at 64,
-// where a tile's step takes as long for half the bytes, 143 / 147 us (13), 150 / 120 us (20),
-// 236 / 179 us (156).
+// front pays late, and the sooner the longer the contexts.  One chunk of 100 to 700 among 20 to
+// 200 tokens, all rows in tiles / shared, longest / mean in brackets: at head size 128, contexts
+// of 500 to 3000 keys, 106 / 117 us (52), 149 / 154 (80), 182 / 185 (97), 224 / 216 (116), 285 /
+// 269 (156); level at 63 with 2000 to 8000 keys, at 70 with 100 to 1000.  At 64, where a tile's
+// step takes as long for half the bytes, 36 / 47 us (17), 60 / 62 (29), 86 / 80 (52), 122 / 101
+// (80); with 2000 to 8000 keys 91 / 82 (17), 148 / 117 (29); with 100 to 1000 25 / 29 (17), 62 /
+// 66 (63), 73 / 68 (80).
 bool is_mixed(const attn::paged::PagedParams& p, int max_q_len, int D) {
     // of a batch padded with empty sequences no more have rows than there are rows beside the longest's
     const long long n = max_q_len < p.total_q ? std::min(p.n_seqs, p.total_q - max_q_len + 1) : p.n_seqs;

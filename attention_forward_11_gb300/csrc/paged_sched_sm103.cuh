@@ -10,9 +10,10 @@
 // T.  All shares are equal for any mixture of lengths, which is what a batch of few long
 // and many short sequences needs.  A stretch that ends inside a unit leaves a piece: the
 // unnormalised sums (m, l, O) of some of its key tiles in fp32, which go to the workspace
-// and are joined by paged_combine_kernel.  Cuts that would leave a piece of less than
-// kMinPiece key tiles move to the unit's edge, and no more blocks than units take part
-// where their shares would be below kMinShare tiles.
+// and are joined by the last block to finish one (paged_rows_kernel: count_piece below, then
+// join_pieces) or by a kernel behind (paged_tiles_kernel: paged_combine_kernel).  Cuts that
+// would leave a piece of less than kMinPiece key tiles move to the unit's edge, and no more
+// blocks than units take part where their shares would be below kMinShare tiles.
 //
 // With d = keys - rows of a sequence, row block i (of t tokens, the last one aside) sees
 // max(0, d + (i + 1) t) keys, an arithmetic series: the length of any number of row
@@ -245,7 +246,10 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
                 sh.blocks = static_cast<int>(n_units);
             } else {
                 // a block for every unit, and more where that leaves shares of kMinShare tiles
-                // (but not a few more, which would cut every unit for little)
+                // (but not for up to half as many more, which cuts units for little: one long sequence
+                // among short ones, blocks / units 1.22, 1.41, 1.47: cut / not 9.2 / 9.1, 10.6 / 11.0,
+                // 9.7 / 12.0 us, and 20.0 / 19.2 at 1.46 in the tiles kernel; 1.6, 2.5, 3.9: 10.5 / 11.0,
+                // 10.4 / 12.6, 10.3 / 15.6)
                 sh.total = total;
                 const long long most_blocks = quotient(total, kTile * kMinShare);
                 sh.blocks = static_cast<int>(min(G, 2 * most_blocks >= 3 * n_units ? most_blocks : n_units));

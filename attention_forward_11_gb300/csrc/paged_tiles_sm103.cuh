@@ -16,10 +16,13 @@
 //     memory before they hand over the weights of a sequence's last tile.
 //   - A warp of its own walks the block's share (paged_sched_sm103.cuh) and posts the
 //     pieces in a ring of kItems work items, so that no role waits for a length.
+//   - P is rounded to the operands' type for its product, as in the dense forward: the tensor
+//     cores take it in 16 bits.  Against 64 bits O is off by 2.1 to 2.4e-3 of its norm in bf16,
+//     2.9e-4 in fp16; O's own rounding alone is 1.7e-3 and 2.1e-4.
 //   - Rows of a tile that are no rows of the sequence are not stored: O goes through
 //     shared memory to rows of 16-byte stores instead of a TMA store.
-// Two prompts of 8192 (32/8 heads of 128) take 694 us, 1585 TFLOP/s, and 512 tokens on 32256
-// cached ones (64/8 heads) 349 us, 1561 TFLOP/s, where the dense forward of the same shapes
+// Two prompts of 8192 (32/8 heads of 128) take 688 us, 1598 TFLOP/s, and 512 tokens on 32256
+// cached ones (64/8 heads) 347 us, 1573 TFLOP/s, where the dense forward of the same shapes
 // takes 666 and 343 us: 2640 SM cycles a key tile of two row tiles against 2520, of which
 // the products are 2048, at the clock that the power cap leaves (1.65 to 1.8 GHz).
 //
@@ -45,7 +48,8 @@ constexpr int kMaskRing = 8;    // page masks of the last K tiles
 constexpr int kItemReaders = kSoftmaxWarps + 4 + 2;  // warps that read an item
 
 // Registers a thread, of the launch's 4 x 128: the epilogue's row addresses take more than
-// the dense forward's, its softmax can spare them (no spills at head size 128).
+// the dense forward's, its softmax can spare them (4 bytes of spills at head size 128, 20 at
+// 64; a version without the first and with 12 of the second is as fast).
 constexpr int kTilesRegsSoftmax = 168, kTilesRegsEpilogue = 96, kTilesRegsOther = 80;
 static_assert(2 * kTilesRegsSoftmax + kTilesRegsEpilogue + kTilesRegsOther <= 4 * (65536 / kThreads),
               "register split exceeds the launch allocation");

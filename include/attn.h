@@ -280,7 +280,8 @@ attn_status_t attn_paged_append(const void* k, const void* v, const long long* s
  *              values past max_pages * page_size as that.
  * block_table, k_cache, v_cache, n_pages .. head_stride  the cache, as above.
  * max_q_len    the longest sequence's rows, >= 1, as far as the host knows.  It chooses
- *              the kernel (few rows against many); results are right for any value.
+ *              the kernel (few rows against many; total_q or more: not known); results are
+ *              right for any value.
  * causal       0: every key of the sequence is visible.  1: row t of a sequence with n
  *              rows and m keys sees keys j <= t + (m - n).  A row that sees no key gets
  *              O = 0 and LSE = -inf.  What unseen rows of the cache hold (stale rows
