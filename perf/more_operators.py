@@ -328,7 +328,7 @@ def _prepare_fwd(case, s, g):
     s["lse"] = torch.zeros((Hq, T), dtype=F32, device="cuda")
     if own:
         import attention_forward_11_gb300 as fa
-        size = fa.attn_paged4_fwd_workspace_size(T, s["max_q_len"], Hq, Hkv, D, page)
+        size = fa.attn_paged_coded_fwd_workspace_size(T, s["max_q_len"], Hq, Hkv, D, page)
         s["workspace"] = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
     return s
 
@@ -351,10 +351,10 @@ def run(s):
             fa.attn_paged_copy(s["copies"], s["caches"])
             return s["all"]
         if op == "append":
-            fa.attn_paged4_append(s["k"], s["v"], s["slot_map"], s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"],
+            fa.attn_paged_coded_append(s["k"], s["v"], s["slot_map"], s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"],
                                   k_unit=case["k_unit"], v_unit=case["v_unit"])
             return s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"]
-        return fa.attn_paged4_fwd(s["q"], s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"], s["block_table"],
+        return fa.attn_paged_coded_fwd(s["q"], s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"], s["block_table"],
                                   s["cu_q"], s["kv_lens"], max_q_len=s["max_q_len"], causal=case["causal"],
                                   scale=s["scale"], k_unit=case["k_unit"], v_unit=case["v_unit"], o=s["o"], lse=s["lse"],
                                   workspace=s["workspace"])
