@@ -15,4 +15,6 @@ from ._binding import (  # noqa: F401
     exported_symbols, attn_bwd, attn_bwd_ptr, attn_bwd_workspace_size,
     attn_paged_tables, attn_paged_tables_ptr, attn_paged_append, attn_paged_append_ptr, attn_paged_fwd,
     attn_paged_fwd_ptr, attn_paged_fwd_workspace_size,
+    attn_paged_fork, attn_paged_fork_ptr, attn_paged_free, attn_paged_free_ptr, attn_paged_copy, attn_paged_copy_ptr,
+    attn_paged_coded_append, attn_paged_coded_append_ptr, attn_paged_coded_fwd, attn_paged_coded_fwd_ptr, attn_paged_coded_fwd_workspace_size,
 )

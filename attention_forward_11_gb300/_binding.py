@@ -27,7 +27,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_splitkv", "attn_fwd_splitkv_wor
             "attn_check_device_status",
             "attn_kernel_launches", "attn_debug_wait_timeout", "attn_bwd", "attn_bwd_workspace_size",
             "attn_debug_unit_rates", "attn_debug_unit_schedule", "attn_paged_tables", "attn_paged_append",
-            "attn_paged_fwd", "attn_paged_fwd_workspace_size")
+            "attn_paged_fwd", "attn_paged_fwd_workspace_size", "attn_paged_fork", "attn_paged_free", "attn_paged_copy",
+            "attn_paged_coded_append", "attn_paged_coded_fwd", "attn_paged_coded_fwd_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +104,19 @@ def load_library():
         lib.attn_paged_fwd.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, L, L, L, L, L, I,
                                        ctypes.c_float, I, P, ctypes.c_size_t, P]
         lib.attn_paged_fwd.restype = I
+        lib.attn_paged_fork.argtypes = [P, P, P, I, I, P, I, P, P, I, L, P, I, P, P, P]
+        lib.attn_paged_fork.restype = I
+        lib.attn_paged_free.argtypes = [P, P, I, I, P, I, L, P, I, P, I, P, P, P]
+        lib.attn_paged_free.restype = I
+        lib.attn_paged_copy.argtypes = [P, I, P, I, I, I, I, I, L, L, L, P]
+        lib.attn_paged_copy.restype = I
+        F = ctypes.c_float
+        lib.attn_paged_coded_append.argtypes = [P] * 7 + [I] * 5 + [L] * 8 + [F, F, I, P]
+        lib.attn_paged_coded_append.restype = I
+        lib.attn_paged_coded_fwd_workspace_size.argtypes = [I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+        lib.attn_paged_coded_fwd_workspace_size.restype = I
+        lib.attn_paged_coded_fwd.argtypes = [P] * 10 + [I] * 9 + [L] * 8 + [I, F, F, F, I, P, ctypes.c_size_t, P]
+        lib.attn_paged_coded_fwd.restype = I
         _lib = lib
         return lib
 
@@ -559,6 +573,287 @@ def _paged_fwd(torch, handle, q, k_cache, v_cache, block_table, cu_q, kv_lens, m
                             workspace.nbytes, handle)
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_fwd")
+    return o, lse
+
+
+# ---- pages that several sequences share
+
+def attn_paged_fork_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return (_lib or load_library()).attn_paged_fork(*args)
+
+
+def attn_paged_free_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return (_lib or load_library()).attn_paged_free(*args)
+
+
+def attn_paged_copy_ptr(*args) -> int:
+    """Raw C-ABI call (pointers as ints, the header's order); returns the status."""
+    return (_lib or load_library()).attn_paged_copy(*args)
+
+
+def attn_paged_fork(parents, kv_lens, free_pages, block_table, page_size: int, shares, lens=None, free_head=None,
+                    copies=None, counts=None, stream=None):
+    """Rows that begin with the tokens of another row (beams, common beginnings of requests).
+
+    parents: int32 [n_seqs], the row that each row takes its first tokens from; outside
+    [0, n_seqs) or itself: none.  lens: int32 [n_seqs], how many (None: all).  kv_lens: int32
+    [n_seqs], tokens of every row, updated in place.  free_pages, free_head: as attn_paged_tables.
+    block_table: int32 [n_seqs, max_pages], updated in place.  shares: int32 [n_pages], rows beyond
+    the first that name a page, updated in place (zeros where nothing is shared yet).
+    Returns (copies int32 [n_seqs, 3] for attn_paged_copy, counts int32 [4]: forks, next free_head,
+    missing pages, rows whose parent has one itself, which are left); allocated here if None.
+    """
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(parents, kv_lens, free_pages, block_table, shares, lens, free_head, copies, counts)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return _paged_fork(torch, torch._C._cuda_getCurrentRawStream(device), parents, kv_lens, free_pages, block_table,
+                           page_size, shares, lens, free_head, copies, counts)
+    with _on(device, stream) as handle:
+        return _paged_fork(torch, handle, parents, kv_lens, free_pages, block_table, page_size, shares, lens, free_head,
+                           copies, counts)
+
+
+def _paged_fork(torch, handle, parents, kv_lens, free_pages, block_table, page_size, shares, lens, free_head, copies,
+                counts):
+    i32, n = torch.int32, parents.numel()
+    n_free, n_pages = free_pages.numel(), shares.numel()
+    _check_ints("parents", parents, i32, n)
+    _check_ints("kv_lens", kv_lens, i32, n)
+    _check_ints("free_pages", free_pages, i32, n_free)
+    _check_ints("shares", shares, i32, n_pages)
+    if lens is not None:
+        _check_ints("lens", lens, i32, n)
+    if free_head is not None:
+        _check_ints("free_head", free_head, i32, 1)
+    max_pages, table_stride = _table_shape(block_table, n, i32)
+    if copies is None:
+        copies = torch.empty((n, 3), dtype=i32, device=parents.device)
+    elif copies.dtype is not i32 or copies.shape != (n, 3) or not copies.is_contiguous():
+        _bad("copies", "a contiguous int32 [n_seqs, 3] tensor")
+    if counts is None:
+        counts = torch.empty(4, dtype=i32, device=parents.device)
+    else:
+        _check_ints("counts", counts, i32, 4)
+    st = attn_paged_fork_ptr(parents.data_ptr(), 0 if lens is None else lens.data_ptr(), kv_lens.data_ptr(), n, page_size,
+                             free_pages.data_ptr(), n_free, 0 if free_head is None else free_head.data_ptr(),
+                             block_table.data_ptr(), max_pages, table_stride, shares.data_ptr(), n_pages,
+                             copies.data_ptr(), counts.data_ptr(), handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_fork")
+    return copies, counts
+
+
+def attn_paged_free(kv_lens, keep_lens, block_table, page_size: int, shares, free_pages, free_head, counts=None,
+                    stream=None):
+    """Pages of rows that end or are cut shorter go back to the free list.
+
+    kv_lens, keep_lens: int32 [n_seqs], tokens that a row has and keeps.  block_table: int32
+    [n_seqs, max_pages] (read).  shares: int32 [n_pages], updated in place.  free_pages: int32
+    [n_free], the list of attn_paged_tables, whose entries before free_head (int32 [1], read) have been
+    taken: the freed pages become the entries in front of it, in ascending order.  Returns counts int32
+    [4]: pages listed, next free_head, pages without room, rows cut inside a shared page; allocated
+    here if None.
+    """
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(kv_lens, keep_lens, block_table, shares, free_pages, free_head, counts)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return _paged_free(torch, torch._C._cuda_getCurrentRawStream(device), kv_lens, keep_lens, block_table, page_size,
+                           shares, free_pages, free_head, counts)
+    with _on(device, stream) as handle:
+        return _paged_free(torch, handle, kv_lens, keep_lens, block_table, page_size, shares, free_pages, free_head, counts)
+
+
+def _paged_free(torch, handle, kv_lens, keep_lens, block_table, page_size, shares, free_pages, free_head, counts):
+    i32, n = torch.int32, kv_lens.numel()
+    n_free, n_pages = free_pages.numel(), shares.numel()
+    _check_ints("kv_lens", kv_lens, i32, n)
+    _check_ints("keep_lens", keep_lens, i32, n)
+    _check_ints("shares", shares, i32, n_pages)
+    _check_ints("free_pages", free_pages, i32, n_free)
+    _check_ints("free_head", free_head, i32, 1)
+    max_pages, table_stride = _table_shape(block_table, n, i32)
+    if counts is None:
+        counts = torch.empty(4, dtype=i32, device=kv_lens.device)
+    else:
+        _check_ints("counts", counts, i32, 4)
+    st = attn_paged_free_ptr(kv_lens.data_ptr(), keep_lens.data_ptr(), n, page_size, block_table.data_ptr(), max_pages,
+                             table_stride, shares.data_ptr(), n_pages, free_pages.data_ptr(), n_free,
+                             free_head.data_ptr(), counts.data_ptr(), handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_free")
+    return counts
+
+
+def attn_paged_copy(copies, caches, stream=None) -> None:
+    """Copy the first tokens of pages to other pages, in many caches at once, in place.
+
+    copies: int32 [n, 3] (from page, to page, tokens), as attn_paged_fork returns them; entries without
+    a page or tokens are skipped.  caches: the tensors [n_pages, page_size, Hkv, x] of all layers, K
+    and V, codes and scales: any element type and strides with the last axis contiguous.  Those of one
+    layout are copied by one kernel (for every 256 of them).
+    """
+    torch = _torch or _load_torch()
+    caches = list(caches)
+    if not caches:
+        _bad("caches", "at least one tensor")
+    device = _on_one_gpu(copies, *caches)
+    if copies.dtype is not torch.int32 or copies.dim() != 2 or copies.shape[1] != 3 or not copies.is_contiguous():
+        _bad("copies", "a contiguous int32 [n, 3] tensor")
+    layouts = {}
+    for c in caches:
+        layouts.setdefault((c.shape, c.stride(), c.dtype), []).append(c.data_ptr())
+    calls = []
+    n_pages, page_size = caches[0].shape[:2] if caches[0].dim() == 4 else (0, 0)
+    for (shape, stride, dtype), ptrs in layouts.items():
+        if len(shape) != 4 or shape[0] != n_pages or shape[1] != page_size or (stride[3] != 1 and shape[3] > 1):
+            _bad("caches", "[n_pages, page_size, heads, x] of one number and size of pages, the last axis contiguous")
+        size = dtype.itemsize
+        calls.append((copies.data_ptr(), copies.shape[0], (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), n_pages, page_size,
+                      shape[2], shape[3] * size, *(x * size for x in stride[:3])))
+    if stream is None and torch._C._cuda_getDevice() == device:
+        _paged_copy(calls, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with _on(device, stream) as handle:
+            _paged_copy(calls, handle)
+
+
+def _paged_copy(calls, handle):
+    for args in calls:
+        st = attn_paged_copy_ptr(*args, handle)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_paged_copy")
+
+
+# ---- paged cache in 4 bits
+
+def _cache4_shape(torch, k_codes, k_scales, v_codes, v_scales):
+    """(n_pages, page_size, Hkv, D) and the strides of the codes and of the scales, in bytes."""
+    u8, e4m3, shape, small = torch.uint8, torch.float8_e4m3fn, k_codes.shape, k_scales.shape
+    if len(shape) != 4 or k_codes.dtype is not u8 or v_codes.dtype is not u8 or v_codes.shape != shape:
+        _bad("k_codes and v_codes", "uint8 [n_pages, page_size, Hkv, D / 2] of one shape")
+    n_pages, page_size, Hkv, half = shape
+    if (k_scales.dtype is not e4m3 and k_scales.dtype is not u8) or (v_scales.dtype is not e4m3 and v_scales.dtype is not u8) or \
+            small != (n_pages, page_size, Hkv, half // 8) or v_scales.shape != small or half % 8 != 0:
+        _bad("k_scales and v_scales", "float8_e4m3fn or uint8 [n_pages, page_size, Hkv, D / 16]")
+    out = []
+    for name, a, b in (("codes", k_codes, v_codes), ("scales", k_scales, v_scales)):
+        stride, other = a.stride(), b.stride()
+        if stride[3] != 1 or (other != stride and any(n > 1 and x != y for n, x, y in zip(a.shape, stride, other))):
+            _bad("k_%s and v_%s" % (name, name), "of one layout, the last axis contiguous")
+        out += stride[:3]
+    return n_pages, page_size, Hkv, 2 * half, out
+
+
+def attn_paged_coded_append_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return (_lib or load_library()).attn_paged_coded_append(*args)
+
+
+def attn_paged_coded_fwd_ptr(*args) -> int:
+    """Raw C-ABI call (device pointers as ints, the header's order); returns the status."""
+    return (_lib or load_library()).attn_paged_coded_fwd(*args)
+
+
+def attn_paged_coded_append(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, k_unit: float = 1.0, v_unit: float = 1.0,
+                       stream=None) -> None:
+    """Write the rows of k and v (bf16 or float16 [T, Hkv, D], heads contiguous, any row stride) in 4 bits
+    into slots slot_map[t] (int64 [T], rows outside the cache skipped), in place.
+
+    k_codes, v_codes: uint8 [n_pages, page_size, Hkv, D / 2], two e2m1 a byte, the first in the low half;
+    k_scales, v_scales: float8_e4m3fn (or uint8) [n_pages, page_size, Hkv, D / 16], one for 16 elements; any
+    strides with the last axis contiguous.  An element is code * scale * unit.
+    """
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(k, v, slot_map, k_codes, k_scales, v_codes, v_scales)
+    n_pages, page_size, Hkv, D, strides = _cache4_shape(torch, k_codes, k_scales, v_codes, v_scales)
+    dtype, shape = k.dtype, k.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        _bad("k and v", "bf16 or float16")
+    if v.dtype is not dtype or v.shape != shape:
+        _bad("v", "of k's type and shape")
+    k_stride, v_stride = _row_stride("k", shape, k.stride(), Hkv, D), _row_stride("v", shape, v.stride(), Hkv, D)
+    T = shape[0]
+    _check_ints("slot_map", slot_map, torch.int64, T)
+    args = (k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+            v_scales.data_ptr(), T, Hkv, D, n_pages, page_size, k_stride, v_stride, *strides, k_unit, v_unit,
+            ATTN_DTYPE_F16 if dtype is torch.float16 else ATTN_DTYPE_BF16)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        st = attn_paged_coded_append_ptr(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with _on(device, stream) as handle:
+            st = attn_paged_coded_append_ptr(*args, handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_coded_append")
+
+
+def attn_paged_coded_fwd_workspace_size(total_q: int, max_q_len: int, Hq: int, Hkv: int, D: int, page_size: int) -> int:
+    """Workspace bytes attn_paged_coded_fwd needs on the current device."""
+    n = ctypes.c_size_t(0)
+    st = int(load_library().attn_paged_coded_fwd_workspace_size(total_q, max_q_len, Hq, Hkv, D, page_size, ctypes.byref(n)))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_coded_fwd_workspace_size")
+    return int(n.value)
+
+
+def attn_paged_coded_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, max_q_len: int | None = None,
+                    causal: int = 1, scale: float | None = None, k_unit: float = 1.0, v_unit: float = 1.0, o=None,
+                    lse=None, workspace=None, stream=None, want_lse: bool = True):
+    """attn_paged_fwd over a cache in 4 bits (attn_paged_coded_append's).
+
+    q, block_table, cu_q, kv_lens, max_q_len, causal, scale, o, lse, workspace and what is returned are as
+    there (the workspace of attn_paged_coded_fwd_workspace_size bytes); the cache and its units as in
+    attn_paged_coded_append.
+    """
+    torch = _torch or _load_torch()
+    device = _on_one_gpu(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, o, lse, workspace)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return _paged4_fwd(torch, torch._C._cuda_getCurrentRawStream(device), q, k_codes, k_scales, v_codes, v_scales,
+                           block_table, cu_q, kv_lens, max_q_len, causal, scale, k_unit, v_unit, o, lse, workspace, want_lse)
+    with _on(device, stream) as handle:
+        return _paged4_fwd(torch, handle, q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, max_q_len,
+                           causal, scale, k_unit, v_unit, o, lse, workspace, want_lse)
+
+
+def _paged4_fwd(torch, handle, q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, max_q_len, causal,
+                scale, k_unit, v_unit, o, lse, workspace, want_lse):
+    dtype, i32, shape = q.dtype, torch.int32, q.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        _bad("q", "bf16 or float16")
+    n_pages, page_size, Hkv, D, strides = _cache4_shape(torch, k_codes, k_scales, v_codes, v_scales)
+    n = kv_lens.numel()
+    _check_ints("kv_lens", kv_lens, i32, n)
+    _check_ints("cu_q", cu_q, i32, n + 1)
+    if len(shape) != 3:
+        _bad("q", "[T, Hq, D]")
+    T, Hq, _ = shape
+    q_stride = _row_stride("q", shape, q.stride(), Hq, D)
+    max_pages, table_stride = _table_shape(block_table, n, i32)
+    if o is None:
+        o = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+    elif o.dtype is not dtype or o.shape != shape or not o.is_contiguous():
+        _bad("o", "a contiguous [T, Hq, D] tensor of q's type")
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
+            _bad("lse", "a contiguous float32 [Hq, T] tensor")
+    elif want_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if max_q_len is None:
+        max_q_len = T
+    if workspace is None:
+        size = attn_paged_coded_fwd_workspace_size(T, max_q_len, Hq, Hkv, D, page_size)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        _bad("workspace", "contiguous")
+    st = attn_paged_coded_fwd_ptr(q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                             o.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                             kv_lens.data_ptr(), n, T, max_q_len, Hq, Hkv, D, n_pages, page_size, max_pages, q_stride,
+                             table_stride, *strides, causal, D ** -0.5 if scale is None else scale, k_unit, v_unit,
+                             ATTN_DTYPE_F16 if dtype is torch.float16 else ATTN_DTYPE_BF16, workspace.data_ptr(),
+                             workspace.nbytes, handle)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_coded_fwd")
     return o, lse
 
 

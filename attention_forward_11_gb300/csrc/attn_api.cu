@@ -20,6 +20,9 @@
 #include "fmha_fwd_d256_sm103.cuh"
 #include "fmha_bwd_d256_sm103.cuh"
 #include "fmha_fwd_sm103.cuh"
+#include "paged4_append_sm103.cuh"
+#include "paged4_rows_sm103.cuh"
+#include "paged_pages_sm103.cuh"
 #include "paged_rows_sm103.cuh"
 #include "paged_sched_sm103.cuh"
 #include "paged_tables_sm103.cuh"
@@ -881,3 +884,5 @@ extern "C" attn_status_t attn_debug_unit_rates(double* out, int n, cudaStream_t 
 }
 
 #include "paged_api.cuh"
+#include "paged_pages_api.cuh"
+#include "paged4_api.cuh"

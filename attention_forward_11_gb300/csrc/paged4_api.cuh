@@ -1,0 +1,238 @@
+// paged4_api.cuh -- host side of the paged cache in 4 bits: argument checks and launches of
+// attn_paged_coded_append and attn_paged_coded_fwd.  Included by attn_api.cu behind paged_api.cuh and
+// paged_pages_api.cuh, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// A cache in 4 bits: strides in bytes.
+struct Cache4 {
+    const void *k_codes, *k_scales, *v_codes, *v_scales;
+    int n_pages, page_size, Hkv, D;
+    long long code_page, code_token, code_head, scale_page, scale_token, scale_head;
+    float k_unit, v_unit;
+    size_t code_bytes() const { return extent(code_page, code_token, code_head, D / 2); }
+    size_t scale_bytes() const { return extent(scale_page, scale_token, scale_head, D / 16); }
+    size_t extent(long long ps, long long ts, long long hs, int row) const {
+        return (size_t)(n_pages - 1) * ps + (size_t)(page_size - 1) * ts + (size_t)(Hkv - 1) * hs + row;
+    }
+};
+
+bool unit_ok(float unit) { return std::isfinite(unit) && unit > 0.f && std::isfinite(1.f / unit); }
+
+attn_status_t check_cache4(Cache4& c) {
+    if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales) return ATTN_ERR_INVALID_ARG;
+    if (c.n_pages < 1 || c.page_size < 1 || c.Hkv < 1 || c.D < 1) return ATTN_ERR_INVALID_ARG;
+    if (c.D != 64 && c.D != 128 && c.D != 256) return ATTN_ERR_UNSUPPORTED;
+    if (!unit_ok(c.k_unit) || !unit_ok(c.v_unit)) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {c.k_codes, c.v_codes})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {c.k_scales, c.v_scales})
+        if (!aligned(ptr, c.D / 16)) return ATTN_ERR_INVALID_ARG;
+    return layout_ok(c.n_pages, c.page_size, c.Hkv, c.D / 2, 16, c.code_page, c.code_token, c.code_head) &&
+                   layout_ok(c.n_pages, c.page_size, c.Hkv, c.D / 16, c.D / 16, c.scale_page, c.scale_token, c.scale_head)
+               ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+template <int kD, int kNB>
+bool opt_in_smem_rows4() {
+    return cudaFuncSetAttribute(attn::paged::paged4_rows_kernel<kD, kNB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                attn::paged::Rows4Geo<kD, kNB>::kSmemBytes) == cudaSuccess;
+}
+
+bool paged4_device_setup(int dev, int* sm_count) {
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    if (!paged_device_setup(dev, sm_count)) return false;  // checks dev
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev])
+        done[dev] = opt_in_smem_rows4<64, 1>() && opt_in_smem_rows4<64, 2>() && opt_in_smem_rows4<64, 3>() &&
+                    opt_in_smem_rows4<64, 4>() && opt_in_smem_rows4<128, 1>() && opt_in_smem_rows4<128, 2>() &&
+                    opt_in_smem_rows4<128, 3>() && opt_in_smem_rows4<256, 1>() && opt_in_smem_rows4<256, 2>();
+    return done[dev];
+}
+
+template <int kD, int kNB>
+attn_status_t launch_rows4(const attn::paged::Paged4Params& p, void* workspace, int sms, cudaStream_t stream) {
+    using namespace attn::paged;
+    using G = Rows4Geo<kD, kNB>;
+    SchedParams sp{};
+    sp.map = make_row_map(p.Hkv, p.group, G::kRows, 1);
+    sp.ws = split_workspace(workspace, sms, G::kRows);
+    sp.tag = next_tag();
+    return launch_behind(paged4_rows_kernel<kD, kNB>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
+}
+
+size_t paged4_workspace_bytes(int sms, long long rows, int D) {
+    return attn::paged::ws_bytes(sms, 8 * row_blocks_for(rows, D), D);
+}
+
+// The variant for sequences of at most `rows` rows.
+template <int kD>
+attn_status_t launch_paged4(const attn::paged::Paged4Params& p, long long rows, void* workspace, int sms, cudaStream_t stream) {
+    const int nb = row_blocks_for(rows, kD);
+    if (nb == 1) return launch_rows4<kD, 1>(p, workspace, sms, stream);
+    if constexpr (kD != 256)
+        if (nb == 3) return launch_rows4<kD, 3>(p, workspace, sms, stream);
+    if constexpr (kD == 64)
+        if (nb == 4) return launch_rows4<kD, 4>(p, workspace, sms, stream);
+    return launch_rows4<kD, 2>(p, workspace, sms, stream);
+}
+
+}  // namespace
+
+extern "C" attn_status_t attn_paged_coded_append(const void* k, const void* v, const long long* slot_map, void* k_codes,
+                                            void* k_scales, void* v_codes, void* v_scales, int n_tokens, int Hkv, int D,
+                                            int n_pages, int page_size, long long k_stride, long long v_stride,
+                                            long long code_page_stride, long long code_token_stride,
+                                            long long code_head_stride, long long scale_page_stride,
+                                            long long scale_token_stride, long long scale_head_stride, float k_unit,
+                                            float v_unit, int dtype, cudaStream_t stream) {
+    if (!k || !v || !slot_map || n_tokens < 1) return ATTN_ERR_INVALID_ARG;
+    Cache4 c{k_codes, k_scales, v_codes, v_scales, n_pages, page_size, Hkv, D, code_page_stride, code_token_stride,
+             code_head_stride, scale_page_stride, scale_token_stride, scale_head_stride, k_unit, v_unit};
+    const attn_status_t st = check_cache4(c);
+    if (st != ATTN_OK) return st;
+    if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F16) return ATTN_ERR_INVALID_ARG;
+    const long long row = (long long)Hkv * D;
+    for (long long stride : {k_stride, v_stride})
+        if (stride % 8 != 0 || stride < row || stride > (1ll << 60) / n_tokens) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return ATTN_ERR_INVALID_ARG;
+    // The caches overlap no row and no slot.  Parts of one interleaved tensor share an address
+    // range without sharing a byte, so they are not compared with one another.
+    const size_t codes = c.code_bytes(), scales = c.scale_bytes();
+    const Range in[3] = {{k, ((size_t)(n_tokens - 1) * k_stride + row) * 2}, {v, ((size_t)(n_tokens - 1) * v_stride + row) * 2},
+                         {slot_map, (size_t)n_tokens * 8}};
+    for (const Range& out : {Range{k_codes, codes}, Range{v_codes, codes}, Range{k_scales, scales}, Range{v_scales, scales}})
+        for (const Range& x : in)
+            if (ranges_overlap(out.at, out.n, x.at, x.n)) return ATTN_ERR_INVALID_ARG;
+    const void* base[4] = {k_codes, v_codes, k_scales, v_scales};
+    for (int a = 0; a < 4; ++a)
+        for (int b = a + 1; b < 4; ++b)
+            if (base[a] == base[b]) return ATTN_ERR_INVALID_ARG;
+    if (row / 16 > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+    attn::paged::Append4Params p{};
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.k_codes = static_cast<uint8_t*>(k_codes);
+    p.k_scales = static_cast<uint8_t*>(k_scales);
+    p.v_codes = static_cast<uint8_t*>(v_codes);
+    p.v_scales = static_cast<uint8_t*>(v_scales);
+    p.slot_map = slot_map;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.code_page = c.code_page;
+    p.code_token = c.code_token;
+    p.code_head = c.code_head;
+    p.scale_page = c.scale_page;
+    p.scale_token = c.scale_token;
+    p.scale_head = c.scale_head;
+    p.n_slots = (long long)n_pages * page_size;
+    p.k_inv = static_cast<float>(1.0 / static_cast<double>(k_unit));
+    p.v_inv = static_cast<float>(1.0 / static_cast<double>(v_unit));
+    p.T = n_tokens;
+    p.row_blocks = static_cast<int>(row / 16);
+    p.head_blocks_log2 = D == 64 ? 2 : D == 128 ? 3 : 4;
+    p.per_block = std::max(1, attn::paged::kAppend4Threads / p.row_blocks);
+    p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
+    p.by_row = attn::paged::make_fastdiv(static_cast<unsigned int>(p.row_blocks));
+    const dim3 blocks(static_cast<unsigned int>(((long long)n_tokens + p.per_block - 1) / p.per_block));
+    return dtype == ATTN_DTYPE_F16
+               ? launch_behind(attn::paged::paged4_append_kernel<true>, blocks, attn::paged::kAppend4Threads, 0, stream, p)
+               : launch_behind(attn::paged::paged4_append_kernel<false>, blocks, attn::paged::kAppend4Threads, 0, stream, p);
+}
+
+extern "C" attn_status_t attn_paged_coded_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
+                                                        size_t* bytes) {
+    if (!bytes) return ATTN_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (total_q < 1 || max_q_len < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)total_q * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !paged4_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
+    *bytes = paged4_workspace_bytes(sms, (long long)max_q_len * (Hq / Hkv), D);
+    return ATTN_OK;
+}
+
+extern "C" attn_status_t attn_paged_coded_fwd(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                                         const void* v_scales, void* o, float* lse, const int* block_table,
+                                         const int* cu_q, const int* kv_lens, int n_seqs, int total_q, int max_q_len,
+                                         int Hq, int Hkv, int D, int n_pages, int page_size, int max_pages,
+                                         long long q_stride, long long table_stride, long long code_page_stride,
+                                         long long code_token_stride, long long code_head_stride,
+                                         long long scale_page_stride, long long scale_token_stride,
+                                         long long scale_head_stride, int causal, float scale, float k_unit,
+                                         float v_unit, int dtype, void* workspace, size_t workspace_bytes,
+                                         cudaStream_t stream) {
+    // ---- validation: nothing is launched on any error
+    if (!q || !o || !block_table || !cu_q || !kv_lens) return ATTN_ERR_INVALID_ARG;
+    if (total_q < 1 || max_q_len < 1 || Hq < 1 || !table_ok(n_seqs, max_pages, table_stride)) return ATTN_ERR_INVALID_ARG;
+    Cache4 c{k_codes, k_scales, v_codes, v_scales, n_pages, page_size, Hkv, D, code_page_stride, code_token_stride,
+             code_head_stride, scale_page_stride, scale_token_stride, scale_head_stride, k_unit, v_unit};
+    const attn_status_t st = check_cache4(c);
+    if (st != ATTN_OK) return st;
+    if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    const double scale_log2 = static_cast<double>(scale) * k_unit * 1.4426950408889634;
+    if (!std::isfinite(static_cast<float>(scale_log2)) || !(static_cast<float>(scale_log2) > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F16) return ATTN_ERR_INVALID_ARG;
+    const long long row = (long long)Hq * D;
+    if (q_stride % 8 != 0 || q_stride < row || q_stride > (1ll << 60) / total_q) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {q, (const void*)o})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {(const void*)lse, (const void*)block_table, (const void*)cu_q, (const void*)kv_lens})
+        if (!aligned(ptr, 4)) return ATTN_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
+    if ((long long)total_q * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    // o, lse and the workspace overlap no input and not each other
+    int dev = 0, sms = 0;
+    const size_t codes = c.code_bytes(), scales = c.scale_bytes();
+    const Range in[8] = {{q, ((size_t)(total_q - 1) * q_stride + row) * 2}, {k_codes, codes}, {v_codes, codes},
+                         {k_scales, scales}, {v_scales, scales},
+                         {block_table, ((size_t)(n_seqs - 1) * table_stride + max_pages) * 4},
+                         {cu_q, ((size_t)n_seqs + 1) * 4}, {kv_lens, (size_t)n_seqs * 4}};
+    Range out[3] = {{o, (size_t)total_q * row * 2}, {lse, lse ? (size_t)total_q * Hq * 4 : 0}, {workspace, 0}};
+    if (outputs_overlap(out, in)) return ATTN_ERR_INVALID_ARG;
+    if (cudaGetDevice(&dev) != cudaSuccess || !paged4_device_setup(dev, &sms)) return ATTN_ERR_CUDA;
+    const long long rows = (long long)max_q_len * (Hq / Hkv);
+    const size_t need = paged4_workspace_bytes(sms, rows, D);
+    if (!workspace || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+    out[2].n = need;
+    if (outputs_overlap(out, in)) return ATTN_ERR_INVALID_ARG;
+    attn::paged::Paged4Params p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_codes = static_cast<const uint8_t*>(k_codes);
+    p.k_scales = static_cast<const uint8_t*>(k_scales);
+    p.v_codes = static_cast<const uint8_t*>(v_codes);
+    p.v_scales = static_cast<const uint8_t*>(v_scales);
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.table = block_table;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
+    p.n_seqs = n_seqs;
+    p.total_q = total_q;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.group = Hq / Hkv;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.causal = causal;
+    p.max_kv = row_tokens(max_pages, page_size);
+    p.q_stride = q_stride;
+    p.table_stride = table_stride;
+    p.page_stride = c.code_page;
+    p.token_stride = c.code_token;
+    p.head_stride = c.code_head;
+    p.scale_page = c.scale_page;
+    p.scale_token = c.scale_token;
+    p.scale_head = c.scale_head;
+    p.scale_log2 = static_cast<float>(scale_log2);
+    p.v_unit = v_unit;
+    p.f16 = dtype == ATTN_DTYPE_F16;
+    p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
+    if (D == 64) return launch_paged4<64>(p, rows, workspace, sms, stream);
+    if (D == 128) return launch_paged4<128>(p, rows, workspace, sms, stream);
+    return launch_paged4<256>(p, rows, workspace, sms, stream);
+}

@@ -10,20 +10,21 @@ size_t cache_extent(int n_pages, int page_size, int Hkv, int D, long long ps, lo
     return ((size_t)(n_pages - 1) * ps + (size_t)(page_size - 1) * ts + (size_t)(Hkv - 1) * hs + D) * 2;
 }
 
-// Do the three strides lay the cache's rows out without overlap?  Each axis, from the
-// one with the smallest stride up, has to step over all that lies below it.  The stride
-// of an axis of one has no meaning and becomes D.
-bool cache_layout_ok(int n_pages, int page_size, int Hkv, int D, long long& ps, long long& ts, long long& hs) {
-    if (n_pages == 1) ps = D;
-    if (page_size == 1) ts = D;
-    if (Hkv == 1) hs = D;
-    if (ps < 1 || ts < 1 || hs < 1 || ps % 8 != 0 || ts % 8 != 0 || hs % 8 != 0) return false;
+// Do the three strides lay the cache's rows (of `row` units, every stride a multiple of
+// `step`) out without overlap?  Each axis, from the one with the smallest stride up, has to
+// step over all that lies below it.  The stride of an axis of one has no meaning and becomes
+// `row`.
+bool layout_ok(int n_pages, int page_size, int Hkv, int row, int step, long long& ps, long long& ts, long long& hs) {
+    if (n_pages == 1) ps = row;
+    if (page_size == 1) ts = row;
+    if (Hkv == 1) hs = row;
+    if (ps < 1 || ts < 1 || hs < 1 || ps % step != 0 || ts % step != 0 || hs % step != 0) return false;
     struct Axis {
         long long stride;
         int n;
     } a[3] = {{hs, Hkv}, {ts, page_size}, {ps, n_pages}};
     std::sort(a, a + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
-    long long below = D;
+    long long below = row;
     for (const Axis& x : a) {
         if (x.n == 1) continue;
         if (x.stride < below) return false;
@@ -31,6 +32,9 @@ bool cache_layout_ok(int n_pages, int page_size, int Hkv, int D, long long& ps, 
         below = x.stride * (x.n - 1) + below;
     }
     return true;
+}
+bool cache_layout_ok(int n_pages, int page_size, int Hkv, int D, long long& ps, long long& ts, long long& hs) {
+    return layout_ok(n_pages, page_size, Hkv, D, 8, ps, ts, hs);
 }
 
 // Sizes of a cache and of what it is used with.

@@ -311,6 +311,151 @@ attn_status_t attn_paged_fwd(const void* q, const void* k_cache, const void* v_c
                              long long token_stride, long long head_stride, int causal, float scale, int dtype,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Pages that several sequences share.
+ *
+ * shares  device int32 [n_pages], for every page the rows of the block table that name it
+ *         beyond the first: 0 for a page of one row and for a free page, so attn_paged_tables
+ *         needs no count.  A buffer of zeros goes with a table without shared pages.  A page
+ *         that is shared is not written to: attn_paged_fork leaves only full pages shared.
+ */
+
+/*
+ * attn_paged_fork -- rows that begin with the tokens of another row (beams, requests with a
+ * common beginning).
+ *
+ * parents   device int32 [n_seqs]: the row that row i takes its first tokens from.  A value
+ *           outside [0, n_seqs), and i itself, mean none: the row is left as it is.  A row whose
+ *           parent has a parent in the same call is left too, and counted.  Any number of rows
+ *           may have one parent.  The pages that a row named before are not given back: free it
+ *           first.
+ * lens      device int32 [n_seqs]: tokens to take (below zero: none; past the parent's: all), or
+ *           NULL for all of the parent's.
+ * kv_lens   device int32 [n_seqs] (in/out): tokens of every row (clamped to what a row can name);
+ *           a fork's becomes the tokens that it took.
+ * free_pages, n_free, free_head  as attn_paged_tables.
+ * block_table  device int32 [n_seqs, max_pages], row stride table_stride (in/out).  With t tokens
+ *           a fork's first t / page_size columns are its parent's.  A rest of t % page_size tokens
+ *           takes a page of the list, in the order of the rows (-1 once it is used up; without a
+ *           page of the parent's that holds the rest none is taken, and the entry is the
+ *           parent's).  Columns behind are left.
+ * shares    (in/out) one more for every column that a fork shares.
+ * copies    device int32 [n_seqs, 3] (written): (from page, to page, tokens) of a fork with a
+ *           rest, for attn_paged_copy; (-1, -1, 0) for all other rows.
+ * counts    device int32 [4] (written): forks; the entry of free_pages at which the next call
+ *           starts; pages that were missing; rows that were left since their parent has one.
+ *
+ * Asynchronous on `stream`, one kernel, no workspace.  All buffers are 4-byte aligned; no output
+ * overlaps an input or another output.  On any error return nothing was launched.
+ */
+attn_status_t attn_paged_fork(const int* parents, const int* lens, int* kv_lens, int n_seqs, int page_size,
+                              const int* free_pages, int n_free, const int* free_head, int* block_table,
+                              int max_pages, long long table_stride, int* shares, int n_pages, int* copies,
+                              int* counts, cudaStream_t stream);
+
+/*
+ * attn_paged_free -- pages of rows that end or are cut shorter go back to the free list.
+ *
+ * kv_lens, keep_lens  device int32 [n_seqs]: tokens that a row has and that it keeps (0: the row
+ *             ends; as many as it has or more: nothing changes; below zero counts as 0).  The
+ *             columns ceil(keep / page_size) to ceil(kv / page_size) - 1 give up their page.
+ * block_table device int32 [n_seqs, max_pages] (read; entries are left as they are).
+ * shares      (in/out) one less for every column that gives up a page.  A page whose count would
+ *             fall below zero is free and has 0.
+ * free_pages  device int32 [n_free] (in/out): the list of attn_paged_tables, whose entries before
+ *             *free_head (device int32, read; clamped to [0, n_free]) have been taken.  The freed
+ *             pages become the entries in front of it, in ascending order.
+ * counts      device int32 [4] (written): pages that were listed; the entry at which the next call
+ *             starts; freed pages that found no room in front of free_head (the lowest numbers);
+ *             rows cut inside a page that is still shared, which is not to be written to: fork the
+ *             row instead.
+ *
+ * Asynchronous on `stream`, one kernel, no workspace; results do not depend on timing.  All
+ * buffers are 4-byte aligned; no output overlaps an input or another output; every size is at
+ * least 1.  On any error return nothing was launched.
+ */
+attn_status_t attn_paged_free(const int* kv_lens, const int* keep_lens, int n_seqs, int page_size,
+                              const int* block_table, int max_pages, long long table_stride, int* shares,
+                              int n_pages, int* free_pages, int n_free, const int* free_head, int* counts,
+                              cudaStream_t stream);
+
+/*
+ * attn_paged_copy -- the first tokens of pages to other pages, in many caches at once.
+ *
+ * copies    device int32 [n_copies, 3]: (from page, to page, tokens), as attn_paged_fork lists them.
+ *           Entries with a page outside [0, n_pages), with no tokens, or from a page to itself are
+ *           skipped; tokens past page_size count as that.  If a page is written by one entry and
+ *           read or written by another, it holds elements of either afterwards.
+ * caches    host array of n_caches device pointers (every layer's K and V, say), read before the
+ *           call returns: caches of one layout, of any element type.  They overlap no other argument.
+ * row_bytes bytes of a head's row, a multiple of 4 (16-bit caches: 2 D; codes of 4 bits: D / 2; their
+ *           scales: D / 16); a page's tokens together are at most 2^31 - 1 bytes.
+ * page_stride .. head_stride  in bytes, multiples of 4, laying no two rows over each other.
+ *
+ * Every size is at least 1.  Asynchronous on `stream`, one kernel for every 256 caches; on any error
+ * return that is not ATTN_ERR_CUDA nothing was launched.
+ */
+attn_status_t attn_paged_copy(const int* copies, int n_copies, void* const* caches, int n_caches, int n_pages,
+                              int page_size, int Hkv, int row_bytes, long long page_stride,
+                              long long token_stride, long long head_stride, cudaStream_t stream);
+
+/*
+ * Paged cache in 4 bits.
+ *
+ * K and V are each two tensors: codes, of D / 2 bytes a head's row, and scales, of D / 16 bytes.
+ * Byte i of a row's codes holds elements 2 i (low half) and 2 i + 1 (high half) as e2m1 (sign bit, then
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6); byte b of its scales is the e4m3 scale of elements 16 b to 16 b + 15.  An
+ * element is code * scale * unit, the unit being a number for all of K (k_unit) or V (v_unit): 1 serves
+ * rows whose blocks' largest elements lie between 2^-4 and 2688; smaller ones lose precision, larger ones
+ * saturate.  4.5 bits an element.
+ *
+ * Rows lie as in a cache of 16 bits, with strides in bytes: the codes' are multiples of 16, the scales' of
+ * D / 16, and so are the base pointers' addresses.  K and V share the strides.  Pages stored head by head
+ * ([page, head, token, .]) keep the small scales of a head's tokens together and are read fastest.
+ */
+
+/*
+ * attn_paged_coded_append -- attn_paged_append into a cache in 4 bits.
+ *
+ * k, v, slot_map, n_tokens, k_stride, v_stride  as attn_paged_append; dtype is an attn_dtype_t.
+ * With y = x / unit (a product with 1 / unit) a block's scale is max |y| / 6 rounded to the nearest
+ * e4m3, ties to even, at most 448 and at least 2^-9 unless the block is zero; a code is y / scale
+ * rounded to the nearest e2m1, ties to the even code, 6 at most, with y's sign (product and quotients
+ * in fp32).  Of a block with a NaN or an infinity the scale is 448, and those are stored as +-6 (a NaN
+ * as +6).  Units are positive and finite, and so is 1 / unit in fp32.
+ *
+ * Errors and the rest as attn_paged_append.
+ */
+attn_status_t attn_paged_coded_append(const void* k, const void* v, const long long* slot_map, void* k_codes,
+                                 void* k_scales, void* v_codes, void* v_scales, int n_tokens, int Hkv, int D,
+                                 int n_pages, int page_size, long long k_stride, long long v_stride,
+                                 long long code_page_stride, long long code_token_stride,
+                                 long long code_head_stride, long long scale_page_stride,
+                                 long long scale_token_stride, long long scale_head_stride, float k_unit,
+                                 float v_unit, int dtype, cudaStream_t stream);
+
+/*
+ * attn_paged_coded_fwd -- attn_paged_fwd over a cache in 4 bits.
+ *
+ * q, o and lse are bf16 or fp16 and fp32 as there, and so are all other arguments and the workspace (of
+ * attn_paged_coded_fwd_workspace_size bytes).  scale * k_unit * log2(e) is positive and finite in fp32.
+ *
+ * Arithmetic: K and V become fp16 without rounding, and q in bf16 does but for elements below 2^-28 of its
+ * row's largest, which are off by at most 2^-39 of that.  P is rounded to fp16, products and softmax
+ * statistics are fp32, O is rounded to nearest even once.  What unseen rows of the cache hold (scales that
+ * are NaN among them) has no influence.
+ */
+attn_status_t attn_paged_coded_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
+                                             size_t* bytes);
+attn_status_t attn_paged_coded_fwd(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                              const void* v_scales, void* o, float* lse, const int* block_table, const int* cu_q,
+                              const int* kv_lens, int n_seqs, int total_q, int max_q_len, int Hq, int Hkv, int D,
+                              int n_pages, int page_size, int max_pages, long long q_stride, long long table_stride,
+                              long long code_page_stride, long long code_token_stride, long long code_head_stride,
+                              long long scale_page_stride, long long scale_token_stride,
+                              long long scale_head_stride, int causal, float scale, float k_unit, float v_unit,
+                              int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* attn_status_str(attn_status_t status);
 
