@@ -21,7 +21,7 @@ HEADERS = [os.path.join(CSRC, f) for f in ("fmha_fwd_sm103.cuh", "fmha_fwd_d256_
                                           "paged_sched_sm103.cuh", "paged_rows_sm103.cuh",
                                           "paged_tiles_sm103.cuh", "paged_api.cuh", "paged_pages_sm103.cuh",
                                           "paged_pages_api.cuh", "paged4_common_sm103.cuh", "paged4_append_sm103.cuh",
-                                          "paged4_rows_sm103.cuh", "paged4_api.cuh", "unit_rates_sm103.cuh",
+                                          "paged4_rows_sm103.cuh", "paged4_tiles_sm103.cuh", "paged4_api.cuh", "unit_rates_sm103.cuh",
                                           "sm103_ptx.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 OUT = os.path.join(PKG, "libattn.so")

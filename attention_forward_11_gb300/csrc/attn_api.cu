@@ -22,6 +22,7 @@
 #include "fmha_fwd_sm103.cuh"
 #include "paged4_append_sm103.cuh"
 #include "paged4_rows_sm103.cuh"
+#include "paged4_tiles_sm103.cuh"
 #include "paged_pages_sm103.cuh"
 #include "paged_rows_sm103.cuh"
 #include "paged_sched_sm103.cuh"

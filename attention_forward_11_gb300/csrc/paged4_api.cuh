@@ -34,10 +34,17 @@ attn_status_t check_cache4(Cache4& c) {
                ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-template <int kD, int kNB>
+template <int kD, int kNB, bool kMany = false>
 bool opt_in_smem_rows4() {
-    return cudaFuncSetAttribute(attn::paged::paged4_rows_kernel<kD, kNB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                attn::paged::Rows4Geo<kD, kNB>::kSmemBytes) == cudaSuccess;
+    return cudaFuncSetAttribute(attn::paged::paged4_rows_kernel<kD, kNB, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                attn::paged::Rows4Geo<kD, kNB, kMany>::kSmemBytes) == cudaSuccess;
+}
+
+template <bool kF16, int kD>
+bool opt_in_smem_tiles4() {
+    return cudaFuncSetAttribute(attn::paged::paged4_tiles_kernel<kF16, kD>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                attn::paged::Tiles4Geo<kD>::kSmemBytes) == cudaSuccess;
 }
 
 bool paged4_device_setup(int dev, int* sm_count) {
@@ -48,35 +55,94 @@ bool paged4_device_setup(int dev, int* sm_count) {
     if (!done[dev])
         done[dev] = opt_in_smem_rows4<64, 1>() && opt_in_smem_rows4<64, 2>() && opt_in_smem_rows4<64, 3>() &&
                     opt_in_smem_rows4<64, 4>() && opt_in_smem_rows4<128, 1>() && opt_in_smem_rows4<128, 2>() &&
-                    opt_in_smem_rows4<128, 3>() && opt_in_smem_rows4<256, 1>() && opt_in_smem_rows4<256, 2>();
+                    opt_in_smem_rows4<128, 3>() && opt_in_smem_rows4<256, 1>() && opt_in_smem_rows4<256, 2>() &&
+                    opt_in_smem_rows4<64, 1, true>() && opt_in_smem_rows4<128, 1, true>() && opt_in_smem_tiles4<false, 64>() &&
+                    opt_in_smem_tiles4<true, 64>() && opt_in_smem_tiles4<false, 128>() && opt_in_smem_tiles4<true, 128>();
     return done[dev];
 }
 
-template <int kD, int kNB>
+template <int kD, int kNB, bool kMany = false>
 attn_status_t launch_rows4(const attn::paged::Paged4Params& p, void* workspace, int sms, cudaStream_t stream) {
     using namespace attn::paged;
-    using G = Rows4Geo<kD, kNB>;
+    using G = Rows4Geo<kD, kNB, kMany>;
     SchedParams sp{};
     sp.map = make_row_map(p.Hkv, p.group, G::kRows, 1);
-    sp.ws = split_workspace(workspace, sms, G::kRows);
+    sp.ws = split_workspace(workspace, sms * G::kTeams, G::kRows);
     sp.tag = next_tag();
-    return launch_behind(paged4_rows_kernel<kD, kNB>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
+    return launch_behind(paged4_rows_kernel<kD, kNB, kMany>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
 }
+
+// Teams of four warps (paged4_rows_sm103.cuh) pay where most of them find a unit of their own.
+bool many_units(int total_q, int n_seqs, int Hkv, int sms) {
+    return (long long)std::min(total_q, n_seqs) * Hkv >= 4ll * sms;
+}
+
+// Does a call take the tcgen05 kernel?  From more rows a key/value head on than the rows kernel
+// computes together, on pages of any size.
+bool takes_tiles4(long long rows, int D) { return rows > 8 * max_row_blocks(D) && D <= 128; }
 
 size_t paged4_workspace_bytes(int sms, long long rows, int D) {
-    return attn::paged::ws_bytes(sms, 8 * row_blocks_for(rows, D), D);
+    if (takes_tiles4(rows, D)) return attn::paged::ws_bytes(sms, attn::kTiles * attn::kBM, D);
+    const int nb = row_blocks_for(rows, D);
+    return attn::paged::ws_bytes(nb == 1 && D <= 128 ? 4 * sms : sms, 8 * nb, D);
 }
 
-// The variant for sequences of at most `rows` rows.
+// The rows kernel's variant for sequences of at most `rows` rows.
 template <int kD>
-attn_status_t launch_paged4(const attn::paged::Paged4Params& p, long long rows, void* workspace, int sms, cudaStream_t stream) {
+attn_status_t launch_rows4_for(const attn::paged::Paged4Params& p, long long rows, void* workspace, int sms, cudaStream_t stream) {
     const int nb = row_blocks_for(rows, kD);
+    if constexpr (kD != 256)
+        if (nb == 1 && many_units(p.total_q, p.n_seqs, p.Hkv, sms)) return launch_rows4<kD, 1, true>(p, workspace, sms, stream);
     if (nb == 1) return launch_rows4<kD, 1>(p, workspace, sms, stream);
     if constexpr (kD != 256)
         if (nb == 3) return launch_rows4<kD, 3>(p, workspace, sms, stream);
     if constexpr (kD == 64)
         if (nb == 4) return launch_rows4<kD, 4>(p, workspace, sms, stream);
     return launch_rows4<kD, 2>(p, workspace, sms, stream);
+}
+
+template <bool kF16, int kD>
+attn_status_t launch_tiles4(const attn::paged::Paged4Params& p, long long rows, void* workspace, int sms, cudaStream_t stream) {
+    using namespace attn::paged;
+    using T = Tiles4Geo<kD>;
+    EncodeTiledFn fn = encoder();
+    if (!fn) return ATTN_ERR_CUDA;
+    SchedParams sp{};
+    sp.map = make_row_map(p.Hkv, p.group, attn::kBM, attn::kTiles);
+    sp.ws = split_workspace(workspace, sms, T::kRows);
+    TilesParams tp{};
+    tp.tile_tokens = sp.map.tokens / attn::kTiles;
+    tp.q_rows = sp.map.heads * tp.tile_tokens;
+    tp.poll_limit = kDefaultPollLimit;
+    CUtensorMap tm;
+    if (!encode_q_map(fn, &tm, kF16, kD, p, sp.map.heads, tp.tile_tokens)) return ATTN_ERR_CUDA;
+    const attn_status_t st = launch_behind(paged4_tiles_kernel<kF16, kD>, dim3(sms), attn::kThreads, T::kSmemBytes,
+                                           stream, tm, p, sp, tp);
+    if (st != ATTN_OK) return st;
+    const int at_once = kCombineThreads / (kD / 4);
+    const int parts = static_cast<int>((std::min<long long>(rows, T::kRows) + at_once - 1) / at_once);
+    return launch_behind(paged_combine_kernel<kF16, kD, T::kRows, attn::kTiles>, dim3(sms, parts), kCombineThreads, 0,
+                         stream, static_cast<const PagedParams&>(p), sp);
+}
+
+template <int kD>
+attn_status_t launch_paged4(const attn::paged::Paged4Params& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
+    const long long rows = (long long)max_q_len * p.group;
+    if constexpr (kD != 256) {
+        if (takes_tiles4(rows, kD)) {
+            attn::paged::Paged4Params half = p;
+            if (is_mixed(p, max_q_len, kD)) {
+                half.split_rows = 8 * row_blocks_for(p.group, kD);
+                half.take_short = 1;
+                const attn_status_t st = launch_rows4_for<kD>(half, p.group, workspace, sms, stream);
+                if (st != ATTN_OK) return st;
+                half.take_short = 0;
+            }
+            return p.f16 ? launch_tiles4<true, kD>(half, rows, workspace, sms, stream)
+                         : launch_tiles4<false, kD>(half, rows, workspace, sms, stream);
+        }
+    }
+    return launch_rows4_for<kD>(p, rows, workspace, sms, stream);
 }
 
 }  // namespace
@@ -232,7 +298,7 @@ extern "C" attn_status_t attn_paged_coded_fwd(const void* q, const void* k_codes
     p.v_unit = v_unit;
     p.f16 = dtype == ATTN_DTYPE_F16;
     p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
-    if (D == 64) return launch_paged4<64>(p, rows, workspace, sms, stream);
-    if (D == 128) return launch_paged4<128>(p, rows, workspace, sms, stream);
-    return launch_paged4<256>(p, rows, workspace, sms, stream);
+    if (D == 64) return launch_paged4<64>(p, max_q_len, workspace, sms, stream);
+    if (D == 128) return launch_paged4<128>(p, max_q_len, workspace, sms, stream);
+    return launch_paged4<256>(p, max_q_len, workspace, sms, stream);
 }

@@ -28,6 +28,17 @@
 namespace attn {
 namespace paged {
 
+// 16 bytes global -> shared, or 16 zero bytes, of rows of kRow bytes that may lie apart: L2 is not
+// asked for more than a row
+template <int kRow>
+__device__ __forceinline__ void cp_async_row16(uint32_t dst, const void* src, bool there) {
+    if constexpr (kRow >= 128)
+        cp_async16(dst, src, there);
+    else if constexpr (kRow == 64)
+        asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 // 4 or 8 bytes global -> shared, or as many zero bytes
 template <int kBytes>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool there) {
@@ -52,20 +63,24 @@ __device__ __forceinline__ void lds_x2(uint32_t* r, uint32_t at) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
 }
 
-template <int kD, int kNB>
+constexpr float kRise = 8.f;  // log2 units
+
+template <int kD, int kNB, bool kMany>
 struct Rows4Geo {
-    static constexpr int kWarps = 8;
-    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kWarps = kMany ? 16 : 8;
+    static constexpr int kTeams = kMany ? 4 : 1;                           // of a block, each with a share of its own
+    static constexpr int kTeamWarps = kWarps / kTeams;
+    static constexpr int kThreads = 32 * kWarps, kTeamThreads = 32 * kTeamWarps;
     static constexpr int kRows = 8 * kNB;
     static constexpr int kKS = kD == 256 ? 1 : 2;       // 16-key blocks of a warp's slice
     static constexpr int kSlice = 16 * kKS;
-    static constexpr int kTileKeys = kSlice * kWarps;
+    static constexpr int kTileKeys = kSlice * kTeamWarps;  // of a team's step
     static constexpr int kCodeRow = kD / 2, kScaleRow = kD / 16;  // bytes of a key
     static constexpr int kCodeBytes = kSlice * kCodeRow, kScaleBytes = kSlice * kScaleRow;
     // a stage: K codes, V codes, K scales, V scales
     static constexpr int kV = kCodeBytes, kScales = 2 * kCodeBytes, kVScales = kScales + kScaleBytes;
     static constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
-    static constexpr int kStages = kD == 64 ? 6 : 4;
+    static constexpr int kStages = kMany ? (kD == 64 ? 4 : 2) : kD == 64 ? 6 : 4;
     static constexpr int kChunks = kCodeRow / 16;  // 16-byte pieces of a row
     static constexpr int kMergeCols = 64;
     static constexpr int kMergeStride = kMergeCols + 2;  // rows 2 t of a warp, and 2 t + 1, fall into different banks
@@ -74,9 +89,10 @@ struct Rows4Geo {
     static constexpr int kStats = kWarps * kRows * 8;
     static constexpr int kSmemBytes = kRing + kMerge + kStats;
     static_assert(kSmemBytes <= 231000, "ring, merge buffer and static shared memory exceed 227 KB");
-    static_assert(kMerge >= kThreads / (kD / 4) * (kD + 4) * 4, "joined rows do not fit the merge buffer");
+    static_assert(kMerge / kTeams >= kTeamThreads / (kD / 4) * (kD + 4) * 4, "joined rows do not fit the merge buffer");
+    static constexpr int kJoinFly = kWarps == 16 ? 8 : 20;  // pieces in flight, as the registers allow
     static constexpr int kMinPiece = 2, kMinShare = 2, kCutTiles = 8;
-    using ShareT = Share<kTileKeys, kMinPiece, kMinShare>;
+    using ShareT = Share<kTileKeys, kMinPiece, kMinShare, kMany ? 512 : 1024>;
     using CursorT = Cursor<ShareT, kTileKeys>;
     // key of slot r of 16, and the 16-byte piece c of row r's place in the row
     __host__ __device__ static constexpr int perm(int r) {
@@ -88,39 +104,79 @@ struct Rows4Geo {
 };
 
 // q's type is looked at where a unit begins and ends only, so one kernel takes both.
-template <int kD, int kNB>
-__global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
+template <int kD, int kNB, bool kMany>
+__global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
     paged4_rows_kernel(const __grid_constant__ Paged4Params p, const __grid_constant__ SchedParams sp) {
-    using G = Rows4Geo<kD, kNB>;
+    using G = Rows4Geo<kD, kNB, kMany>;
     constexpr int kKS = G::kKS, kStages = G::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_part[3 * G::kWarps];
-    __shared__ StartPos s_start;
+    __shared__ StartPos s_start[G::kTeams];
     __shared__ uint32_t s_valid[G::kWarps][kStages];  // keys of a slice that have a page
-    __shared__ int s_last;
+    __shared__ int s_last[G::kTeams];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
+    const int team = warp / G::kTeamWarps, mate = warp % G::kTeamWarps;
+    const int me = static_cast<int>(blockIdx.x) * G::kTeams + team;  // of all teams
+    const int ttid = tid % G::kTeamThreads;
+    auto meet = [&]() {  // of the team
+        if constexpr (G::kTeams == 1) __syncthreads();
+        else named_bar_sync(1 + team, G::kTeamThreads);
+    };
     const uint32_t ring = smem_u32(smem) + warp * (kStages * G::kStageBytes);
-    float* merge = reinterpret_cast<float*>(smem + G::kRing);
-    float2* stats = reinterpret_cast<float2*>(smem + G::kRing + G::kMerge);
+    float* merge = reinterpret_cast<float*>(smem + G::kRing + team * (G::kMerge / G::kTeams));
+    float2* stats = reinterpret_cast<float2*>(smem + G::kRing + G::kMerge + team * (G::kStats / G::kTeams));
     launch_dependents();
     touch_params(p);
     touch_params(sp);
     wait_for_primary();
 
-    typename G::ShareT sh;
-    const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare, G::kCutTiles, false>(p, sp, s_part, &s_start, sh);
-    if (!some) return;
-    typename G::CursorT cur;
-    cur.first(p, sp, sh, s_start);
-    typename G::CursorT ld = cur;  // the copies' position, ahead of the products'
-    int ld_tile = ld.tile;
-    // the counts of the pieces at this share's ends (ready before any is counted)
-    CountWord counts[2];
-    if (tid == G::kThreads - 1) {
-        counts[0] = look_at_count(sp.ws.count(static_cast<int>(blockIdx.x)));
-        counts[1] = look_at_count(sp.ws.count(cur.ok && cur.tile > 0 ? sh.starter(cur.at) : static_cast<int>(blockIdx.x)));
+    // The share and the two positions in it are looked at where a unit begins or ends only; kept in
+    // registers they would take a third of a thread's.
+    __shared__ typename G::ShareT s_sh[G::kTeams];
+    __shared__ typename G::CursorT s_cur[G::kWarps], s_ld[G::kWarps];  // of the products, and of the copies ahead of them
+    {
+        typename G::ShareT sh;
+        const bool some = find_share<G::kThreads, typename G::ShareT, G::kTileKeys, G::kMinShare, G::kCutTiles, false, G::kTeams>(
+            p, sp, s_part, s_start, sh, team);
+        if (!some || sh.begin == sh.end) return;  // the team's warps: they meet nobody but one another
+        typename G::CursorT first;
+        first.first(p, sp, sh, s_start[team]);
+        if (ttid == 0) s_sh[team] = sh;
+        if (lane == 0) s_cur[warp] = s_ld[warp] = first;
+        // the counts of the pieces at this share's ends are made ready before any is counted
+        if (ttid == G::kTeamThreads - 1) {
+            const CountWord a = look_at_count(sp.ws.count(me));
+            const CountWord b = look_at_count(sp.ws.count(first.ok && first.tile > 0 ? sh.starter(first.at) : me));
+            begin_count(a, sp.tag);
+            if (b.word != a.word) begin_count(b, sp.tag);
+        }
+        meet();
     }
+    auto advance = [&](typename G::CursorT* at) {
+        typename G::CursorT c = *at;
+        c.next(p, sp, s_sh[team]);
+        __syncwarp();
+        if (lane == 0) *at = c;
+        __syncwarp();
+    };
+    // where the copies are
+    struct Ahead {
+        const int* row;  // of the table
+        int tile, tile_end, keys, hkv;
+        bool ok;
+    } ld;
+    auto take = [&]() {
+        const typename G::CursorT& c = s_ld[warp];
+        ld.ok = c.ok;
+        if (!c.ok) return;
+        ld.row = p.table + c.s * p.table_stride;
+        ld.tile = c.tile;
+        ld.tile_end = c.tile_end;
+        ld.keys = c.keys;
+        ld.hkv = sp.map.kv_head(c.head_unit);
+    };
+    take();
 
     // The page numbers of the next slices to copy: lane i has that of key i % kSlice.  A slice
     // is looked up when the one before it is copied, the first ones together.
@@ -135,34 +191,33 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
         k.row = 0;
         k.ok = ld.ok;
         if (!ld.ok) return;
-        const int key = ld_tile * G::kTileKeys + G::kSlice * warp + (lane & (G::kSlice - 1));
-        k.some = ld_tile * G::kTileKeys + G::kSlice * warp < ld.keys;
-        k.hkv = sp.map.kv_head(ld.head_unit);
+        const int first = ld.tile * G::kTileKeys + G::kSlice * mate, key = first + (lane & (G::kSlice - 1));
+        k.some = first < ld.keys;
+        k.hkv = ld.hkv;
         if (key < ld.keys) {
             const int col = static_cast<int>(p.by_page.quot(key));
-            k.page = p.table[ld.s * p.table_stride + col];
+            k.page = ld.row[col];
             k.row = key - col * p.page_size;
         }
-        if (++ld_tile == ld.tile_end) {
-            ld.next(p, sp, sh);
-            ld_tile = ld.tile;
+        if (++ld.tile == ld.tile_end) {
+            advance(&s_ld[warp]);
+            take();
         }
     };
     // Copies a slice into a stage.  A lane has 16 bytes of every (32 / kChunks)-th row of codes,
     // and the scales of a row.
     constexpr int kRowsAtOnce = 32 / G::kChunks;
     const int lane_row = lane / G::kChunks, lane_chunk = lane % G::kChunks;
-    const long long lane_at = lane_row * p.token_stride + lane_chunk * 16;
     const bool blocks_in_pages = p.page_size % 16 == 0;
     auto copy = [&](const Look& k, int st) {
         if (k.ok) {
             const bool there = k.page >= 0 && k.page < p.n_pages;
-            const long long page = there ? k.page : 0;
-            const long long base = page * p.page_stride + k.row * p.token_stride + k.hkv * p.head_stride;
             const uint32_t valid = __ballot_sync(0xffffffffu, there);
-            if (lane == 0) s_valid[warp][st] = valid;
+            const uint32_t to = ring + st * G::kStageBytes;
             if (k.some) {
-                const uint32_t to = ring + st * G::kStageBytes;
+                if (lane == 0) s_valid[warp][st] = valid;
+                const long long page = there ? k.page : 0;
+                const long long base = page * p.page_stride + k.row * p.token_stride + k.hkv * p.head_stride;
                 const long long scales = page * p.scale_page + k.row * p.scale_token + k.hkv * p.scale_head;
                 if constexpr (kKS == 2) {
                     cp_async_small<G::kScaleRow>(to + G::kScales + lane * G::kScaleRow, p.k_scales + scales, there);
@@ -174,6 +229,7 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                 auto place = [&](int row) { return to + row * G::kCodeRow + G::place(row, lane_chunk) * 16; };
                 if (blocks_in_pages && valid == 0xffffffffu) {
                     // 16 keys of one page each
+                    const long long lane_at = lane_row * p.token_stride + lane_chunk * 16;
 #pragma unroll
                     for (int b = 0; b < kKS; ++b) {
                         const long long at = __shfl_sync(0xffffffffu, base, 16 * b) + lane_at;
@@ -181,8 +237,8 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 16; i += kRowsAtOnce) {
                             const uint32_t dst = place(16 * b + lane_row + i);
-                            cp_async16(dst, pk);
-                            cp_async16(dst + G::kV, pv);
+                            cp_async_row16<G::kCodeRow>(dst, pk, true);
+                            cp_async_row16<G::kCodeRow>(dst + G::kV, pv, true);
                             pk += kRowsAtOnce * p.token_stride;
                             pv += kRowsAtOnce * p.token_stride;
                         }
@@ -194,8 +250,8 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                         const bool ok = (valid >> row) & 1;
                         const long long from = __shfl_sync(0xffffffffu, base, row);
                         const long long at = ok ? from + lane_chunk * 16 : 0;
-                        cp_async16(place(row), p.k_codes + at, ok);
-                        cp_async16(place(row) + G::kV, p.v_codes + at, ok);
+                        cp_async_row16<G::kCodeRow>(place(row), p.k_codes + at, ok);
+                        cp_async_row16<G::kCodeRow>(place(row) + G::kV, p.v_codes + at, ok);
                     }
                 }
             }
@@ -211,19 +267,21 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) copy(first[i], i);
     }
-    if (tid == G::kThreads - 1) {
-        begin_count(counts[0], sp.tag);
-        if (counts[1].word != counts[0].word) begin_count(counts[1], sp.tag);
-    }
     int st = 0;
 
 #pragma unroll 1
-    for (; cur.ok; cur.next(p, sp, sh)) {
-        const Seq x = cur.x;
-        const int t0 = cur.row_unit * sp.map.tokens;
+    for (; s_cur[warp].ok; advance(&s_cur[warp])) {
         // Q^T as the products' B operand: row n0 + g, elements 4 j to 4 j + 3 of this lane's quarter
         uint32_t qf[kNB][kD / 16][2];
         float back[kNB];  // what undoes the row's factor
+        int lim[kNB][2], all_see = 0x7fffffff;  // keys that each of this thread's rows sees, and that every row sees
+        float m[kNB][2], l[kNB][2], sl2[kNB][2], o[kNB][kD / 16][4];
+        int tile, tile_end, keys;
+        {
+        const typename G::CursorT& cur = s_cur[warp];
+        const Seq x = cur.x;
+        const int t0 = cur.row_unit * sp.map.tokens;
+        tile = cur.tile, tile_end = cur.tile_end, keys = cur.keys;
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
             const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + g);
@@ -252,8 +310,6 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
             }
         }
         // this thread's two rows of every row block: 2 t4 and 2 t4 + 1
-        int lim[kNB][2], all_see = 0x7fffffff;  // keys that every row sees
-        float m[kNB][2], l[kNB][2], sl2[kNB][2], o[kNB][kD / 16][4];
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
@@ -265,6 +321,7 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                 l[nb][e] = 0.f;
                 sl2[nb][e] = p.scale_log2 * __shfl_sync(0xffffffffu, back[nb], (2 * t4 + e) * 4);
             }
+        }
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, d));
 #pragma unroll
@@ -275,15 +332,15 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                 for (int e = 0; e < 4; ++e) o[nb][j][e] = 0.f;
 
 #pragma unroll 1
-        for (int tile = cur.tile; tile < cur.tile_end; ++tile) {
+        for (; tile < tile_end; ++tile) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // the slice is there, and every lane is done with the one before
             copy(next, st == 0 ? kStages - 1 : st - 1);
             look_up(next);
-            const int k0 = tile * G::kTileKeys + G::kSlice * warp;
+            const int k0 = tile * G::kTileKeys + G::kSlice * mate;
             const uint32_t from = ring + st * G::kStageBytes;
             const uint32_t valid = s_valid[warp][st];
-            if (k0 < cur.keys) {
+            if (k0 < keys) {
                 float sc[kNB][kKS][4];
 #pragma unroll
                 for (int b = 0; b < kKS; ++b) {
@@ -340,33 +397,28 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                 uint32_t pf[kNB][kKS][2];
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
-                    // element e of block b: slot g + 8 (e / 2), row 2 t4 + e % 2
-                    float al[2];
+                    // element e of block b: slot g + 8 (e / 2), row 2 t4 + e % 2.  The maximum that weights
+                    // are relative to rises when a logit is past it by more than kRise: weights are at
+                    // most 2^kRise, and most slices only look.
+                    float mx[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = -INFINITY;
+                        mx[e] = fmaxf(sc[nb][0][e], sc[nb][0][2 + e]);
 #pragma unroll
-                        for (int b = 0; b < kKS; ++b)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) mx = fmaxf(mx, sc[nb][b][2 * u + e]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        const float mn = fmaxf(m[nb][e], mx * sl2[nb][e]), use = mn == -INFINITY ? 0.f : mn;
-                        al[e] = ex2_approx(m[nb][e] - use);
-                        m[nb][e] = mn;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int b = 0; b < kKS; ++b)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                float& y = sc[nb][b][2 * u + e];
-                                y = ex2_approx(fmaf(y, sl2[nb][e], -use));
-                                sum += y;
-                            }
-                        l[nb][e] = l[nb][e] * al[e] + sum;
+                        for (int b = 1; b < kKS; ++b) mx[e] = fmaxf(mx[e], fmaxf(sc[nb][b][e], sc[nb][b][2 + e]));
+                        mx[e] *= sl2[nb][e];
                     }
-                    // the maximum settles after a few slices: most leave O as it is
-                    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+                    if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + kRise || mx[1] > m[nb][1] + kRise)) {
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+                            const float mn = fmaxf(m[nb][e], mx[e]);
+                            al[e] = ex2_approx(m[nb][e] - (mn == -INFINITY ? 0.f : mn));
+                            m[nb][e] = mn;
+                            l[nb][e] *= al[e];
+                        }
 #pragma unroll
                         for (int j = 0; j < kD / 16; ++j) {
                             o[nb][j][0] *= al[0];
@@ -374,6 +426,18 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                             o[nb][j][2] *= al[0];
                             o[nb][j][3] *= al[1];
                         }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float use = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+#pragma unroll
+                        for (int b = 0; b < kKS; ++b)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float& y = sc[nb][b][2 * u + e];
+                                y = ex2_approx(fmaf(y, sl2[nb][e], -use));
+                                l[nb][e] += y;
+                            }
                     }
 #pragma unroll
                     for (int b = 0; b < kKS; ++b) {
@@ -430,35 +494,38 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
-                if (g == 0) stats[warp * G::kRows + 8 * nb + 2 * t4 + e] = make_float2(m[nb][e], l[nb][e]);
+                if (g == 0) stats[mate * G::kRows + 8 * nb + 2 * t4 + e] = make_float2(m[nb][e], l[nb][e]);
             }
+        const typename G::CursorT& cur = s_cur[warp];
+        const Seq x = cur.x;
+        const int t0 = cur.row_unit * sp.map.tokens;
         const bool whole = cur.whole();
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (cur.tile == 0 ? 1 : 0);
+        const int slot = 2 * me + (cur.tile == 0 ? 1 : 0);
         constexpr int kParts = kD / G::kMergeCols;  // of a row: products 4 part to 4 part + 3 of every lane
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
-                __syncthreads();  // the stats are there; what was merged before has been read
+                meet();  // the stats are there; what was merged before has been read
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)  // row 2 t4 + e lies at 4 e + t4
-                        *reinterpret_cast<float2*>(merge + (warp * 8 + 4 * e + t4) * G::kMergeStride + 8 * g + 2 * j) =
+                        *reinterpret_cast<float2*>(merge + (mate * 8 + 4 * e + t4) * G::kMergeStride + 8 * g + 2 * j) =
                             make_float2(o[nb][4 * part + j][e], o[nb][4 * part + j][2 + e]);
-                __syncthreads();
+                meet();
 #pragma unroll
-                for (int i = tid; i < 8 * (G::kMergeCols / 2); i += G::kThreads) {
+                for (int i = ttid; i < 8 * (G::kMergeCols / 2); i += G::kTeamThreads) {
                     const int at = i / (G::kMergeCols / 2), r = 2 * (at & 3) + (at >> 2);
                     const int dc = (i % (G::kMergeCols / 2)) * 2, d = (kD / 8) * (dc >> 3) + 8 * part + (dc & 7);
                     const Row w = row_of(p, sp.map, x, cur.head_unit, t0, sp.map.tokens, 8 * nb + r);
                     if (!w.there) continue;
                     float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
-                    for (int k = 0; k < G::kWarps; ++k) M = fmaxf(M, stats[k * G::kRows + 8 * nb + r].x);
+                    for (int k = 0; k < G::kTeamWarps; ++k) M = fmaxf(M, stats[k * G::kRows + 8 * nb + r].x);
                     const float use = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                    for (int k = 0; k < G::kWarps; ++k) {
+                    for (int k = 0; k < G::kTeamWarps; ++k) {
                         const float2 ml = stats[k * G::kRows + 8 * nb + r];
                         const float f = ex2_approx(ml.x - use);
                         const float2 v = *reinterpret_cast<const float2*>(merge + (k * 8 + at) * G::kMergeStride + dc);
@@ -483,17 +550,17 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB>::kThreads, 1)
                     }
                 }
             }
-        __syncthreads();  // the stats may be overwritten; a piece is written
+        meet();  // the stats may be overwritten; a piece is written
         if (!whole) {
-            const int first = cur.tile == 0 ? static_cast<int>(blockIdx.x) : sh.starter(cur.at);
-            const int n = sh.pieces(cur.at, cur.tiles, first);
-            if (tid == 0) s_last = count_piece(sp.ws.count(first), n);
-            __syncthreads();
-            if (s_last) {
-                if (p.f16) join_pieces<true, kD, G::kRows, G::kThreads>(p, sp, x, cur.head_unit, t0, first, n, merge);
-                else join_pieces<false, kD, G::kRows, G::kThreads>(p, sp, x, cur.head_unit, t0, first, n, merge);
+            const int first = cur.tile == 0 ? me : s_sh[team].starter(cur.at);
+            const int n = s_sh[team].pieces(cur.at, cur.tiles, first);
+            if (ttid == 0) s_last[team] = count_piece(sp.ws.count(first), n);
+            meet();
+            if (s_last[team]) {
+                if (p.f16) join_pieces<true, kD, G::kRows, G::kTeamThreads, G::kJoinFly>(p, sp, x, cur.head_unit, t0, first, n, merge, G::kTeams == 1 ? 0 : 1 + team);
+                else join_pieces<false, kD, G::kRows, G::kTeamThreads, G::kJoinFly>(p, sp, x, cur.head_unit, t0, first, n, merge, G::kTeams == 1 ? 0 : 1 + team);
             }
-            __syncthreads();
+            meet();
         }
     }
     cp_async_wait<0>();

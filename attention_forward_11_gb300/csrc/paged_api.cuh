@@ -166,6 +166,17 @@ size_t paged_workspace_bytes(int sms, long long rows, int D, int page_size) {
     return attn::paged::ws_bytes(sms, takes_tiles(rows, D, page_size) ? attn::kTiles * attn::kBM : 8 * row_blocks_for(rows, D), D);
 }
 
+// Tensor map of q: boxes of 64 columns x `heads` heads x `tokens` tokens.
+bool encode_q_map(EncodeTiledFn fn, CUtensorMap* tm, bool f16, int D, const attn::paged::PagedParams& p, int heads, int tokens) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.total_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens}, estr[3] = {1, 1, 1};
+    return fn(tm, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kF16, int kD>
 attn_status_t launch_tiles(const attn::paged::PagedParams& p, long long rows, void* workspace, int sms,
                            cudaStream_t stream) {
@@ -185,14 +196,8 @@ attn_status_t launch_tiles(const attn::paged::PagedParams& p, long long rows, vo
     const CUtensorMapDataType type = kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapL2promotion promotion =
         kD == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUtensorMap tm[3];
-    const cuuint64_t q_dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.Hq, (cuuint64_t)p.total_q};
-    const cuuint64_t q_strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)p.q_stride * 2};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)sp.map.heads, (cuuint32_t)tp.tile_tokens};
-    if (fn(&tm[0], type, 3, const_cast<uint16_t*>(p.q), q_dims, q_strides, q_box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return ATTN_ERR_CUDA;
+    if (!encode_q_map(fn, &tm[0], kF16, kD, p, sp.map.heads, tp.tile_tokens)) return ATTN_ERR_CUDA;
     // K and V: boxes of box_rows rows.  A row of head size 128 is two 128-byte halves of a
     // swizzled tile, which a tensor map of (64 columns, row, head, page) copies apart.  With
     // the axes (64 columns, 8 rows, half, 8-row group, page) one box has both, and a head is

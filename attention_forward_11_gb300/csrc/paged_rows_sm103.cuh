@@ -117,14 +117,15 @@ struct RowsGeo {
 // Joins the n pieces of a unit that block `first` started: M = max m, L = sum l 2^(m - M),
 // O = sum O 2^(m - M) / L.  kD / 4 threads have a row (four columns each), or, when there are
 // fewer rows than such groups, a part of a row's pieces; `buf` is shared scratch of a row and
-// its sum for every group.  A block does this alone at its end, so what counts is how many
-// loads wait on one another: 20 pieces are in flight at once, the first before M is known.
-template <bool kF16, int kD, int kRows, int kThreads>
+// its sum for every group.  `bar`: the threads are a team of their block with that barrier.  A block does this alone at its end, so what counts is how many
+// loads wait on one another: kFly pieces are in flight at once, the first before M is known.
+template <bool kF16, int kD, int kRows, int kThreads, int kFly = 20>
 __device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedParams& sp, const Seq& x, int head_unit, int t0,
-                                            int first, int n, float* buf) {
-    constexpr int kLanes = kD / 4, kGroups = kThreads / kLanes, kFly = 20;
+                                            int first, int n, float* buf, int bar = 0) {
+    constexpr int kLanes = kD / 4, kGroups = kThreads / kLanes;
     constexpr int kSpan = kLanes < 32 ? kLanes : 32;  // lanes that share a search for M
-    const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4, lane = threadIdx.x % kSpan;
+    const int tid = threadIdx.x % kThreads;
+    const int group = tid / kLanes, col = tid % kLanes * 4, lane = tid % kSpan;
     const int rows = min(min(sp.map.tokens, x.q_len - t0) * sp.map.heads, kRows);
     int parts = 1;
     while (2 * parts * rows <= kGroups) parts *= 2;
@@ -170,7 +171,8 @@ __device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedPar
             float* to = buf + group * (kD + 4);
             *reinterpret_cast<float4*>(to + col) = acc;
             if (col == 0) to[kD] = L;
-            __syncthreads();
+            if (bar == 0) __syncthreads();
+            else named_bar_sync(bar, kThreads);
             if (part == 0)
                 for (int k = 1; k < parts; ++k) {
                     const float* from = buf + (group + k) * (kD + 4);

@@ -27,7 +27,8 @@
 namespace attn {
 namespace paged {
 
-constexpr int kUnitKeys = 256;  // a unit's own cost, in keys (about 2 us of 64 KB tiles)
+constexpr int kUnitKeys = 256;  // a unit's own cost, in keys (about 2 us of 64 KB tiles); kernels
+                                // that take a key in less time have a cost of their own (kUnit)
 
 struct RowMap {
     int heads;      // query heads of a block
@@ -101,6 +102,7 @@ __device__ __forceinline__ int unit_keys(const PagedParams& p, const SchedParams
 }
 
 // Length of the first r row units of a head (r < row_units, or all of them).
+template <int kUnit>
 __device__ __forceinline__ long long units_length(const PagedParams& p, const SchedParams& sp, const Seq& x, int r) {
     long long keys;
     if (!p.causal) {
@@ -112,18 +114,20 @@ __device__ __forceinline__ long long units_length(const PagedParams& p, const Sc
         const long long i0 = d >= 0 ? 0 : min((long long)sp.map.by_tokens.quot(-d), n);   // the first that sees a key: d + (i0 + 1) t > 0
         keys = (n - i0) * d + t * ((n * (n + 1) - i0 * (i0 + 1)) / 2) + (all ? x.kv_len : 0);
     }
-    return keys + (long long)r * kUnitKeys;
+    return keys + (long long)r * kUnit;
 }
 
+template <int kUnit>
 __device__ __forceinline__ long long seq_length(const PagedParams& p, const SchedParams& sp, const Seq& x) {
-    return x.q_len == 0 ? 0 : sp.map.head_units * units_length(p, sp, x, row_units(sp, x));
+    return x.q_len == 0 ? 0 : sp.map.head_units * units_length<kUnit>(p, sp, x, row_units(sp, x));
 }
 
 // A block's share, and a position in it.  kTile: keys of a tile (a power of two).
-template <int kTile, int kMinPiece, int kMinShare>
+template <int kTile, int kMinPiece, int kMinShare, int kUnitCost = kUnitKeys>
 struct Share {
-    // two cuts are at least kUnitKeys (as many blocks as units) or kMinShare tiles apart
-    static_assert(kTile <= kUnitKeys && kMinShare >= 1, "two cuts never fall on one tile");
+    static constexpr int kUnit = kUnitCost;
+    // two cuts are at least kUnit (as many blocks as units) or kMinShare tiles apart
+    static_assert(kTile <= kUnit && kMinShare >= 1, "two cuts never fall on one tile");
     long long begin, end;  // stretch of this block
     long long total;
     int blocks;            // that have a share
@@ -131,22 +135,22 @@ struct Share {
 
     // Tile at which a cut at length `at` of a unit of `tiles` tiles falls.
     __device__ __forceinline__ static int cut(long long at, int tiles) {
-        const long long t = at <= kUnitKeys ? 0 : (at - kUnitKeys) / kTile;
+        const long long t = at <= kUnit ? 0 : (at - kUnit) / kTile;
         if (t < kMinPiece) return 0;
         return tiles - t < kMinPiece ? tiles : static_cast<int>(t);
     }
     // Blocks whose cut falls inside a unit that starts at `start`: those before the first
     // whose cut would be at the unit's end.
     __device__ __forceinline__ int pieces(long long start, int tiles, int first) const {
-        // cut(x) < tiles  <=>  x < kUnitKeys + kTile * (tiles - kMinPiece + 1)
-        const long long y = start + kUnitKeys + (long long)kTile * (tiles - kMinPiece + 1);
+        // cut(x) < tiles  <=>  x < kUnit + kTile * (tiles - kMinPiece + 1)
+        const long long y = start + kUnit + (long long)kTile * (tiles - kMinPiece + 1);
         const long long last = quotient(y * blocks + total - 1, total) - 1;  // largest c with floor(c T / G) < y
         return static_cast<int>(min(last, (long long)blocks - 1)) - first + 1;
     }
     // The block that has the first piece of a cut unit: the first whose end is no cut at
     // the unit's start.
     __device__ __forceinline__ int starter(long long start) const {
-        const long long y = start + kUnitKeys + (long long)kTile * kMinPiece;
+        const long long y = start + kUnit + (long long)kTile * kMinPiece;
         return static_cast<int>(quotient(y * blocks + total - 1, total)) - 1;  // first c with floor((c + 1) T / G) >= y
     }
 };
@@ -173,9 +177,12 @@ __device__ __forceinline__ long long block_sum(long long v, long long* part) {
 
 // The share of block blockIdx.x and the sequence it starts in (block-wide; `part`, three
 // values a warp, and `found` are shared scratch).  Returns false for a block without work.
-template <int kThreads, class ShareT, int kTile, int kMinShare, int kCutTiles, bool kAlign>
+// With kTeams > 1 a block's threads are that many teams, each with a share, `found` and `sh` of
+// its own, as if they were blocks; `team` is the thread's.  A team without work has an empty
+// share (begin == end).
+template <int kThreads, class ShareT, int kTile, int kMinShare, int kCutTiles, bool kAlign, int kTeams = 1>
 __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedParams& sp, long long* part, StartPos* found,
-                                           ShareT& sh) {
+                                           ShareT& sh, int team = 0) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     const bool one_step = p.n_seqs <= kThreads;
@@ -183,7 +190,7 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
     if (!one_step) {
         for (int s = tid; s < p.n_seqs; s += kThreads) {
             const Seq x = seq_of(p, s);
-            total += seq_length(p, sp, x);
+            total += seq_length<ShareT::kUnit>(p, sp, x);
             n_units += row_units(sp, x);
             if (x.q_len > 0) longest = max(longest, (long long)x.kv_len);
         }
@@ -201,7 +208,7 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
         const int s = s0 + tid;
         Seq x{};
         if (s < p.n_seqs) x = seq_of(p, s);
-        const long long len = seq_length(p, sp, x);
+        const long long len = seq_length<ShareT::kUnit>(p, sp, x);
         const int units = row_units(sp, x);
         long long v = len;
         int u = units;
@@ -230,7 +237,7 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
             if (one_step) total = step, n_units = units_step;
             if (total == 0) return false;
             n_units *= sp.map.head_units;
-            const long long c = blockIdx.x, G = gridDim.x;
+            const long long c0 = (long long)blockIdx.x * kTeams, c = c0 + team, G = (long long)gridDim.x * kTeams;
             // Whole units where the longest is no longer than an equal share and what a cut
             // costs at its end (kCutTiles), or, where units share K/V tiles in L2 and need them
             // as fast as L2 gives them (kAlign; whole units all start at key 0 and keep in step),
@@ -239,7 +246,7 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
             // size 128; on 8000 keys 101 / 110, 101 / 100, 99 / 90.  At 64, where a tile's softmax
             // takes longer than its bytes, 294 / 286, 296 / 256, 296 / 226, 294 / 211: no kAlign.
             const long long share = quotient(total, G);
-            longest += kUnitKeys;
+            longest += ShareT::kUnit;
             sh.whole = n_units <= G && (longest <= share + kCutTiles * kTile || (kAlign && longest * 100 <= share * 135));
             if (sh.whole) {
                 sh.total = n_units;
@@ -254,21 +261,36 @@ __device__ __forceinline__ bool find_share(const PagedParams& p, const SchedPara
                 const long long most_blocks = quotient(total, kTile * kMinShare);
                 sh.blocks = static_cast<int>(min(G, 2 * most_blocks >= 3 * n_units ? most_blocks : n_units));
             }
-            if (c >= sh.blocks) return false;
-            sh.begin = quotient(c * sh.total, sh.blocks);
-            sh.end = quotient((c + 1) * sh.total, sh.blocks);
+            if (c0 >= sh.blocks) return false;
+            sh.begin = quotient(min(c, (long long)sh.blocks) * sh.total, sh.blocks);
+            sh.end = quotient(min(c + 1, (long long)sh.blocks) * sh.total, sh.blocks);
         }
         const long long end = sh.whole ? (units_before + u) * sp.map.head_units : before + v;
         const long long start = end - (sh.whole ? (long long)units * sp.map.head_units : len);
-        if (sh.begin >= start && sh.begin < end) {
-            found->seq = s;
-            found->seq_at = start;
-            found->x = x;
+        if constexpr (kTeams == 1) {
+            if (sh.begin >= start && sh.begin < end) {
+                found->seq = s;
+                found->seq_at = start;
+                found->x = x;
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < kTeams; ++t) {
+                const long long c = min((long long)blockIdx.x * kTeams + t, (long long)sh.blocks);
+                const long long begin = quotient(c * sh.total, sh.blocks);
+                if (begin >= start && begin < end) {
+                    found[t].seq = s;
+                    found[t].seq_at = start;
+                    found[t].x = x;
+                }
+            }
         }
         at += step;
         units_at += units_step;
         __syncthreads();
-        if ((sh.whole ? units_at * sp.map.head_units : at) > sh.begin) break;
+        const long long last = kTeams == 1 ? sh.begin
+                                           : quotient(min((long long)(blockIdx.x + 1) * kTeams, (long long)sh.blocks) * sh.total, sh.blocks) - 1;
+        if ((sh.whole ? units_at * sp.map.head_units : at) > last) break;
     }
     return true;
 }
@@ -285,7 +307,7 @@ struct Cursor {
     bool whole_units;
     bool ok;
 
-    __device__ __forceinline__ int length() const { return whole_units ? 1 : keys + kUnitKeys; }
+    __device__ __forceinline__ int length() const { return whole_units ? 1 : keys + ShareT::kUnit; }
     __device__ __forceinline__ bool whole() const { return tile == 0 && tile_end == tiles; }
 
     // The next sequence that has rows, from s on (every lane of a warp calls this).  A batch captured
@@ -346,7 +368,7 @@ struct Cursor {
         ok = true;
         n_row_units = row_units(sp, x);
         whole_units = sh.whole;
-        const long long per_head = sh.whole ? n_row_units : units_length(p, sp, x, n_row_units);
+        const long long per_head = sh.whole ? n_row_units : units_length<ShareT::kUnit>(p, sp, x, n_row_units);
         head_unit = static_cast<int>(quotient(sh.begin - f.seq_at, per_head));
         const long long head_at = f.seq_at + head_unit * per_head, rest = sh.begin - head_at;
         // the last row unit that starts at or before the position: the warp's lanes try 32 at
@@ -355,13 +377,13 @@ struct Cursor {
         int lo = 0, n = n_row_units;  // it is one of [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32, at_lane = lo + lane * step;
-            const bool before = lane * step < n && (sh.whole ? at_lane : units_length(p, sp, x, at_lane)) <= rest;  // lane 0: true
+            const bool before = lane * step < n && (sh.whole ? at_lane : units_length<ShareT::kUnit>(p, sp, x, at_lane)) <= rest;  // lane 0: true
             const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
             n = min(step, n - k * step);
             lo += k * step;
         }
         row_unit = lo;
-        at = head_at + (sh.whole ? lo : units_length(p, sp, x, lo));
+        at = head_at + (sh.whole ? lo : units_length<ShareT::kUnit>(p, sp, x, lo));
         seek(p, sp, sh);
     }
 };
