@@ -11,11 +11,10 @@
 //     warps that are idle between two epilogues otherwise.
 //   - Every lane finds the page of a row of its own, so pages of any size are taken; rows without
 //     a key become zeros, so V needs no clean-up.
-//   - bf16 queries become fp16 in shared memory, and a row's power of two goes into its softmax
-//     scale.
-//   - Fills, conversions of Q and epilogues are one sequence in a fixed order in which nothing
-//     waits for what comes behind it: item j's epilogue runs after the fill of the stage behind
-//     the one with its last V, item j + 1's Q having been converted.
+//   - The softmax warps turn bf16 queries into fp16 in shared memory before their first product; a
+//     row's power of two goes into its softmax scale.
+//   - Fills and epilogues are one sequence in a fixed order in which nothing waits for what comes
+//     behind it: item j's epilogue runs after the fill of the stage behind the one with its last V.
 //
 // Waits are bounded as in the dense forward: after a timeout all roles leave, copies and
 // MMAs in flight are waited for, and tensor memory is freed.
@@ -27,6 +26,7 @@
 
 #include "fmha_fwd_sm103.cuh"
 #include "paged4_common_sm103.cuh"
+#include "paged4_rows_sm103.cuh"
 #include "paged_common_sm103.cuh"
 #include "paged_sched_sm103.cuh"
 #include "paged_tiles_sm103.cuh"
@@ -35,13 +35,8 @@
 namespace attn {
 namespace paged {
 
-// Registers a thread, of the launch's 4 x 128: the fills hold two tiles' codes.
-#ifndef T4_S
-#define T4_S 168
-#define T4_E 112
-#define T4_O 64
-#endif
-constexpr int kTiles4RegsSoftmax = T4_S, kTiles4RegsEpilogue = T4_E, kTiles4RegsOther = T4_O;
+// Registers a thread, of the launch's 4 x 128: the fills take more than the dense forward's epilogue.
+constexpr int kTiles4RegsSoftmax = 168, kTiles4RegsEpilogue = 112, kTiles4RegsOther = 64;
 static_assert(2 * kTiles4RegsSoftmax + kTiles4RegsEpilogue + kTiles4RegsOther <= 4 * (65536 / kThreads),
               "register split exceeds the launch allocation");
 
@@ -80,8 +75,10 @@ struct Tiles4Geo {
     static constexpr int kSmemQ = 0;
     static constexpr int kSmemK = kSmemQ + kTiles * kTileBytes;
     static constexpr int kSmemV = kSmemK + kStages * kTileBytes;
-    static constexpr int kSmemStage = kSmemV + kStages * kTileBytes;  // O staging: 4 KB a warp
-    static constexpr int kSmemStats = kSmemStage + kHalfBytes;        // per tile and row: (m, l)
+    // codes of the next K tile and of the next V tile, 16 bytes a thread and row, and their scales
+    static constexpr int kCodeBytes = kBM * kD / 2, kScaleBytes = kBM * (kD / 32) * 4;
+    static constexpr int kSmemCodes = kSmemV + kStages * kTileBytes;
+    static constexpr int kSmemStats = kSmemCodes + 2 * (kCodeBytes + kScaleBytes);  // per tile and row: (m, l)
     static constexpr int kSmemBar = kSmemStats + kTiles * kBM * 8;
     static constexpr int kSmemTmemSlot = kSmemBar + kBarCount * 8;
     static constexpr int kSmemAbort = kSmemTmemSlot + 4;
@@ -91,8 +88,7 @@ struct Tiles4Geo {
     static constexpr int kSmemStart = (kSmemMask + kMaskRing * 4 * kMaskWords + 7) / 8 * 8;
     static constexpr int kSmemPart = kSmemStart + static_cast<int>(sizeof(StartPos));
     static constexpr int kSmemItems = kSmemPart + 3 * (kThreads / 32) * 8;
-    static constexpr int kSmemBack = kSmemItems + kItems * static_cast<int>(sizeof(Item));  // of two items: what undoes a row's factor
-    static constexpr int kSmemUsed = kSmemBack + 2 * kTiles * kBM * 4;
+    static constexpr int kSmemUsed = kSmemItems + kItems * static_cast<int>(sizeof(Item));
     static constexpr int kSmemBytes = kSmemUsed + 1024;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
     static_assert(kStages + 2 < kMaskRing, "a K tile's page mask is read before it is replaced");
@@ -460,13 +456,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nvis = 0;  // visible keys of this row from the item's next key tile on
             if (row_token < tp.tile_tokens && token < w.q_len)
                 nvis = (p.causal ? max(w.kv_len - w.q_len + token + 1, 0) : w.kv_len) - w.kb * kBN;
-            if constexpr (kTurnsQ) {
-                const bool got = wait_bounded(bar(T::kBarQReady + t), j & 1, abort_flag, limit);
+            if constexpr (kTurnsQ) {  // this row of Q_t from bf16 to fp16
+                const bool got = wait_bounded(bar(T::kBarQFull + t), j & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                sl2 = p.scale_log2 * reinterpret_cast<const float*>(smem + T::kSmemBack)[((j & 1) * kTiles + t) * kBM + r];
+                uint8_t* row = smem + T::kSmemQ + t * T::kTileBytes + r * 128;
+                auto piece = [&](int q) { return reinterpret_cast<uint4*>(row + q / 8 * kHalfBytes + ((q % 8) ^ (r & 7)) * 16); };
+                uint4 x[kD / 8];
+                uint32_t top2 = 0;
+#pragma unroll
+                for (int q = 0; q < kD / 8; ++q) {
+                    x[q] = *piece(q);
+                    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(x[q].x & 0x7fff7fffu, x[q].y & 0x7fff7fffu),
+                                                   __vmaxu2(x[q].z & 0x7fff7fffu, x[q].w & 0x7fff7fffu)));
+                }
+                float inverse;
+                const float factor = row_factor(max(top2 & 0xffffu, top2 >> 16), inverse);
+                sl2 = p.scale_log2 * inverse;
+#pragma unroll
+                for (int q = 0; q < kD / 8; ++q)
+                    *piece(q) = make_uint4(bf16x2_to_f16x2(x[q].x, factor), bf16x2_to_f16x2(x[q].y, factor),
+                                           bf16x2_to_f16x2(x[q].z, factor), bf16x2_to_f16x2(x[q].w, factor));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(T::kBarQReady + t));
             }
             float m_run = -INFINITY;  // running max (log2 units of scaled logits) used by the weights
             float l_run = 0.f;        // running sum of weights
@@ -592,7 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp % 4;
         const int r = wq * 32 + lane;  // row within a tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        uint8_t* stage = smem + T::kSmemStage + wq * 4096;  // this warp's 32 rows of 128 bytes
         const int row_token = r / sp.map.heads, row_head = r % sp.map.heads;
         bool ok = true;
         // stores item j's O and LSE, or its piece
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tO = tmem_base + lane_off + kTmemO + 128 * t;
                 const float inv_l = ml.y == 0.f ? 0.f : p.v_unit / ml.y;
                 const size_t ws_row = static_cast<size_t>(w.slot >= 0 ? w.slot : 0) * T::kRows + t * kBM + r;
-                // 32 columns at a time: the fills' registers are in use
+                // A thread stores its row's 32 columns as they come: whole sectors
 #pragma unroll
                 for (int h = 0; h < kD / 32; ++h) {
                     uint32_t o[32];
@@ -633,48 +647,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(bar(T::kBarOFree + t));
                     }
-                    if (w.slot >= 0 && !__any_sync(0xffffffffu, there)) continue;
+                    if (!there) continue;
                     if (w.slot >= 0) {  // a piece: sums to its workspace slot
-                        float* dst = sp.ws.o + (ws_row - lane) * kD + 32 * h;  // of the warp's first row
+                        float4* dst = reinterpret_cast<float4*>(sp.ws.o + ws_row * kD + 32 * h);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            float f[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(o[4 * q + e]) * p.v_unit;
-                            *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                                make_float4(f[0], f[1], f[2], f[3]);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rr = 4 * i + lane / 8, q = lane % 8;
-                            *reinterpret_cast<uint4*>(dst + rr * kD + 4 * q) =
-                                *reinterpret_cast<const uint4*>(stage + rr * 128 + ((q ^ (rr & 7)) * 16));
-                        }
-                        __syncwarp();
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(__uint_as_float(o[4 * q]) * p.v_unit, __uint_as_float(o[4 * q + 1]) * p.v_unit,
+                                                 __uint_as_float(o[4 * q + 2]) * p.v_unit, __uint_as_float(o[4 * q + 3]) * p.v_unit);
                         continue;
                     }
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(out_row) * kD + 32 * h);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // 16-byte chunk q of this row's 64 bytes
+                    for (int q = 0; q < 4; ++q) {
                         float f[8];
 #pragma unroll
                         for (int e = 0; e < 8; e += 2)
                             fmul2_b(f[e], f[e + 1], __uint_as_float(o[8 * q + e]), __uint_as_float(o[8 * q + e + 1]),
                                     inv_l);
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) =
-                            make_uint4(pack_x2<kF16>(f[0], f[1]), pack_x2<kF16>(f[2], f[3]),
-                                       pack_x2<kF16>(f[4], f[5]), pack_x2<kF16>(f[6], f[7]));
+                        dst[q] = make_uint4(pack_x2<kF16>(f[0], f[1]), pack_x2<kF16>(f[2], f[3]),
+                                            pack_x2<kF16>(f[4], f[5]), pack_x2<kF16>(f[6], f[7]));
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // eight rows at a time, four lanes a row
-                        const int rr = 8 * i + lane / 4, q = lane % 4;
-                        const int to = __shfl_sync(0xffffffffu, out_row, rr);
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((q ^ ((rr >> 1) & 3)) * 16));
-                        if (to >= 0)
-                            *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(to) * kD + 32 * h + 8 * q) = x;
-                    }
-                    __syncwarp();
                 }
                 if (there) {
                     if (w.slot >= 0)
@@ -689,80 +681,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kLanes = kD / 32;          // of a row, with 32 elements each
         constexpr int kAtOnce = 32 / kLanes;     // rows of a warp in one step; a warp has rows 32 wq to 32 wq + 31
         const int chunk = lane % kLanes, first_row = 32 * wq + lane / kLanes;
-        float* back = reinterpret_cast<float*>(smem + T::kSmemBack);
-        struct Rows {  // 32 elements of kLanes rows
-            uint4 codes[kLanes];
-            uint32_t scales[kLanes];  // two e4m3
-        };
         // where the rows of a tile lie: this lane's row 32 wq + lane (page < 0: no such key or no page)
         struct Place {
             int page, row;
             uint32_t there, missing;  // rows of this warp that have a page; keys that have none
         };
-        auto load = [&](Rows& x, const Place& at, const uint8_t* codes, const uint8_t* scales, int hkv) {
-            const long long page = max(at.page, 0);
+        // A thread's codes wait in shared memory: registers that loads were in flight for would be
+        // spilled around the epilogue.
+        const uint32_t k_codes = sbase + T::kSmemCodes + r * 16, k_scales = sbase + T::kSmemCodes + T::kCodeBytes + r * 4;
+        constexpr uint32_t kToV = T::kCodeBytes + T::kScaleBytes;
+        auto load = [&](const Place& at, const uint8_t* codes, const uint8_t* scales, int hkv, uint32_t off) {
+            const long long page = at.page;
             const long long code = page * p.page_stride + at.row * p.token_stride + hkv * p.head_stride;
             const long long scale = page * p.scale_page + at.row * p.scale_token + hkv * p.scale_head;
+            long long c[kLanes], b[kLanes];
 #pragma unroll
             for (int i = 0; i < kLanes; ++i) {
-                const int from = i * kAtOnce + lane / kLanes;
-                const long long c = __shfl_sync(0xffffffffu, code, from), b = __shfl_sync(0xffffffffu, scale, from);
-                x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-                x.scales[i] = 0;
-                if ((at.there >> from) & 1) {
-                    x.codes[i] = __ldg(reinterpret_cast<const uint4*>(codes + c) + chunk);
-                    x.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + b) + chunk);
-                }
+                c[i] = __shfl_sync(0xffffffffu, code, i * kAtOnce + lane / kLanes);
+                b[i] = __shfl_sync(0xffffffffu, scale, i * kAtOnce + lane / kLanes);
+            }
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const bool there = (at.there >> (i * kAtOnce + lane / kLanes)) & 1;
+                cp_async_row16<kD / 2>(k_codes + off + i * (kBM * 16), codes + c[i] + chunk * 16, there);
+                cp_async_small<4>(k_scales + off + i * (kBM * 4), scales + b[i] + chunk / 2 * 4, there);
             }
         };
-        // as TMA lays out a swizzled tile of 64-column halves
-        auto store = [&](const Rows& x, uint32_t tile) {
+        // As TMA lays out a swizzled tile of 64-column halves.  The halves of a row fall into the same
+        // banks, so lanes of the second one store their pieces in another order.
+        const uint32_t later = kD == 128 ? chunk / 2 * 2 : 0;  // 0 or 2
+        auto store = [&](uint32_t tile, uint32_t off) {
+            uint32_t w[kLanes][4], two[kLanes];
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                lds_x2(w[i], k_codes + off + i * (kBM * 16) + later * 4);
+                lds_x2(w[i] + 2, k_codes + off + i * (kBM * 16) + (later ^ 2) * 4);
+                two[i] = lds_bytes<2>(k_scales + off + i * (kBM * 4) + chunk % 2 * 2);
+            }
 #pragma unroll
             for (int i = 0; i < kLanes; ++i) {
                 const int row = first_row + i * kAtOnce;
                 const uint32_t to = tile + chunk / 2 * kHalfBytes + row * 128;
-                const uint32_t two = e4m3_to_f16(x.scales[i]), by[2] = {low_twice(two), high_twice(two)};
-                const uint32_t w[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+                const uint32_t s2 = e4m3_to_f16(two[i]);
+                const uint32_t by[2] = {later ? high_twice(s2) : low_twice(s2), later ? low_twice(s2) : high_twice(s2)};
+                uint32_t h[4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t h[4];
-                    e2m1_to_f16(h, w[q]);
+                    e2m1_to_f16(h[q], w[i][q]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], by[q / 2]);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((chunk % 2 * 4 + q) ^ (row & 7)) << 4)),
-                                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                    for (int e = 0; e < 4; ++e) h[q][e] = hmul2(h[q][e], by[q / 2]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + (((chunk % 2 * 4 + (q ^ later)) ^ (row & 7)) << 4)),
+                                 "r"(h[q][0]), "r"(h[q][1]), "r"(h[q][2]), "r"(h[q][3])
                                  : "memory");
-                }
             }
-        };
-        // Q_t of item j: bf16 to fp16
-        auto turn_q = [&](int j) -> bool {
-            for (int t = 0; t < kTiles; ++t) {
-                const bool got = wait_bounded(bar(T::kBarQFull + t), j & 1, abort_flag, limit);
-                if (!__all_sync(0xffffffffu, got)) return false;
-                uint8_t* row = smem + T::kSmemQ + t * T::kTileBytes + r * 128;
-                uint32_t top2 = 0;
-#pragma unroll
-                for (int q = 0; q < kD / 8; ++q) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(row + q / 8 * kHalfBytes + ((q % 8) ^ (r & 7)) * 16);
-                    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                }
-                float inverse;
-                const float factor = row_factor(max(top2 & 0xffffu, top2 >> 16), inverse);
-                back[((j & 1) * kTiles + t) * kBM + r] = inverse;
-#pragma unroll
-                for (int q = 0; q < kD / 8; ++q) {
-                    uint4* at = reinterpret_cast<uint4*>(row + q / 8 * kHalfBytes + ((q % 8) ^ (r & 7)) * 16);
-                    const uint4 x = *at;
-                    *at = make_uint4(bf16x2_to_f16x2(x.x, factor), bf16x2_to_f16x2(x.y, factor),
-                                     bf16x2_to_f16x2(x.z, factor), bf16x2_to_f16x2(x.w, factor));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(T::kBarQReady + t));
-            }
-            return true;
         };
         // The tile whose K is next: `ahead` is one further, for its page numbers to arrive in time.
         struct Tile {
@@ -806,7 +781,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         Tile cur, ahead;
         Place here, next;
-        Rows k, v;
         enter(cur, 0);
         if (cur.ok) {
             look_up(cur, here);
@@ -814,8 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             step_on(ahead);
             look_up(ahead, next);
             settle(cur, here);
-            load(k, here, p.k_codes, p.k_scales, cur.hkv);
+            load(here, p.k_codes, p.k_scales, cur.hkv, 0);
         }
+        cp_async_commit();
         bool have_v = false;
         int ends = -1, pending = -1;  // items whose last V is next, or is in the stage before
         for (int g = 0; ok && (cur.ok || have_v); ++g) {
@@ -825,32 +800,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            const bool had_v = have_v, starts = cur.ok && cur.kt == 0;
-            const int ended = ends, j_here = cur.j;
+            cp_async_wait<0>();
+            const bool had_v = have_v;
+            const int ended = ends;
             if (cur.ok) {
-                store(k, sbase + T::kSmemK + st * T::kTileBytes);
+                store(sbase + T::kSmemK + st * T::kTileBytes, 0);
                 if (lane == 0) page_mask[g % kMaskRing * T::kMaskWords + wq] = here.missing;
             }
-            const Place of_v = here;
-            const int v_hkv = cur.hkv;
-            const bool v_next = cur.ok;
+            if (had_v) store(sbase + T::kSmemV + ((g - 1) % kStages) * T::kTileBytes, kToV);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(T::kBarKvFull + st));
+            // the codes of this tile's V and of the next one's K, and the page numbers of the one behind
+            have_v = cur.ok;
             ends = cur.ok && cur.kt + 1 == cur.n ? cur.j : -1;
-            if (cur.ok) {  // K of the next tile, and the page numbers of the one behind
+            if (cur.ok) {
+                load(here, p.v_codes, p.v_scales, cur.hkv, kToV);
                 cur = ahead;
                 here = next;
                 if (cur.ok) {
                     settle(cur, here);
-                    load(k, here, p.k_codes, p.k_scales, cur.hkv);
+                    load(here, p.k_codes, p.k_scales, cur.hkv, 0);
                     step_on(ahead);
                     look_up(ahead, next);
                 }
             }
-            if (had_v) store(v, sbase + T::kSmemV + ((g - 1) % kStages) * T::kTileBytes);
-            have_v = v_next;
-            if (v_next) load(v, of_v, p.v_codes, p.v_scales, v_hkv);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(T::kBarKvFull + st));
+            cp_async_commit();
             if (pending >= 0) {
                 Item w;
                 if (!look_at_item(pending, w, ok)) break;
@@ -859,12 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 release_item(pending);
             }
             pending = had_v ? ended : -1;
-            if (kTurnsQ && starts && !turn_q(j_here)) ok = false;
         }
         if (ok && pending >= 0) {
             Item w;
             if (look_at_item(pending, w, ok)) finish(pending, w);
         }
+        cp_async_wait<0>();
     }
 
     // ---- teardown: all tensor-memory traffic is complete; free it
