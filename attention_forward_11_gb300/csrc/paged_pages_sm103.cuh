@@ -15,7 +15,8 @@
 // rows gives a shared page its last push depends on timing, so the freed pages are listed by
 // number: the counts are lowered first, then every page whose count is below zero is found by
 // a scan over all counts.  Both halves are one launch of one cluster of 8 blocks, whose
-// hardware barrier stands between them; no workspace, no second launch.
+// hardware barrier stands between them; no workspace.  Where a table is large 8 SMs take longer
+// over its rows than a second launch does, and the first half is a launch over all of them.
 //
 // paged_copy_kernel copies the first tokens of pages to other pages in up to 256 caches (all
 // layers' K and V) at once.
@@ -40,6 +41,7 @@ struct ForkParams {
 };
 
 constexpr int kForkThreads = 1024;  // rows scanned per step
+constexpr int kForkRowWarps = 4, kForkRows = kForkThreads / 32 / kForkRowWarps;  // warps of a row, rows written at a time
 
 __global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const ForkParams p) {
     __shared__ int s_parent[kForkThreads];  // -1: no fork
@@ -90,19 +92,19 @@ __global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const ForkPara
         forks += s_part[1][31] & 0xffffffff;
         refused += s_part[1][31] >> 32;
         __syncthreads();
-        for (int j = warp * G + c; j < n; j += (kForkThreads / 32) * G) {
+        for (int j = warp / kForkRowWarps * G + c; j < n; j += kForkRows * G) {
             const int from = s_parent[j];
             if (from < 0) continue;
             const int full = static_cast<int>(p.by_page.quot(s_len[j]));
             const int* row = p.table + from * p.table_stride;
             int* to = p.table + (s0 + j) * p.table_stride;
 #pragma unroll 4
-            for (int col = lane; col < full; col += 32) {
+            for (int col = warp % kForkRowWarps * 32 + lane; col < full; col += 32 * kForkRowWarps) {
                 const int x = row[col];
                 to[col] = x;
                 if (is_page(x)) atomicAdd(p.shares + x, 1);
             }
-            if (lane == 0 && s_len[j] > full * p.page_size) to[full] = s_last[j];
+            if (lane == 0 && warp % kForkRowWarps == 0 && s_len[j] > full * p.page_size) to[full] = s_last[j];
         }
         __syncthreads();
     }
@@ -121,6 +123,7 @@ struct FreeParams {
     long long table_stride;
     int n_seqs, n_free, n_pages, page_size;
     int max_kv;
+    int phase;  // 0: all in one cluster; 1: the counts are lowered, by the whole GPU; 2: the rest, behind that
     FastDiv by_page;
 };
 
@@ -152,7 +155,8 @@ __global__ void __cluster_dims__(kFreeBlocks, 1, 1) __launch_bounds__(kFreeThrea
         keep = max(p.keep_lens[s], 0);
     };
     // pages behind the kept tokens: one row less names each
-    for (int s = warp * kFreeBlocks + c; s < p.n_seqs; s += kWarps * kFreeBlocks) {
+    const int blocks = gridDim.x;
+    for (int s = p.phase == 2 ? p.n_seqs : warp * blocks + c; s < p.n_seqs; s += kWarps * blocks) {
         int kv, keep;
         lens(s, kv, keep);
         if (keep >= kv) continue;
@@ -165,6 +169,7 @@ __global__ void __cluster_dims__(kFreeBlocks, 1, 1) __launch_bounds__(kFreeThrea
             if (x >= 0 && x < p.n_pages) atomicSub(p.shares + x, 1);
         }
     }
+    if (p.phase == 1) return;
     __threadfence();
     cluster_barrier();
     // what is below zero is free; first how many there are in this block's part of the pages
@@ -265,6 +270,7 @@ struct CopyParams {
     int heads, pieces;  // of a token, of a head's row
     int parts;          // that a page is copied in
     int head_first;     // a head's tokens follow one another more closely than a token's heads
+    int run;            // bytes of a token where a head's tokens follow one another without a gap, or 0
     FastDiv by_token, by_row, by_cache, by_parts;  // heads * pieces, pieces, n_caches, parts
     char* caches[kCopyMaxCaches];
 };
@@ -317,25 +323,42 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const __grid_c
         }
         __syncthreads();
         const long long units = (long long)n * p.n_caches * p.parts;
-        for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        for (long long u = (long long)blockIdx.x * kWarps + warp; u < units; u += (long long)gridDim.x * kWarps) {  // a warp's
             const long long pair = (long long)p.by_parts.quot(u);
             const int part = static_cast<int>(u - pair * p.parts);
             const int which = static_cast<int>(p.by_cache.quot(pair));
             char* base = p.caches[pair - (long long)which * p.n_caches];
             const char* from = base + s_copy[which][0] * p.page_stride;
             char* to = base + s_copy[which][1] * p.page_stride;
-            const unsigned int rows = s_copy[which][2], of_head = rows * p.pieces;
+            // pieces of a head; a run's last one may be a part, copied word by word
+            const unsigned int rows = s_copy[which][2], run = rows * p.run;
+            const unsigned int of_head = p.run != 0 ? (run + sizeof(Piece) - 1) / sizeof(Piece) : rows * p.pieces;
             const unsigned int all = of_head * p.heads;
             const unsigned int end = static_cast<unsigned int>((long long)all * (part + 1) / p.parts);
-            for (unsigned int k = static_cast<unsigned int>((long long)all * part / p.parts) + threadIdx.x; k < end;
-                 k += kCopyFly * kCopyThreads) {
+            for (unsigned int k = static_cast<unsigned int>((long long)all * part / p.parts) + lane; k < end;
+                 k += kCopyFly * 32) {
                 Piece v[kCopyFly];
                 long long at[kCopyFly];
 #pragma unroll
                 for (int j = 0; j < kCopyFly; ++j) {
-                    const unsigned int x = k + j * kCopyThreads;
+                    const unsigned int x = k + j * 32;
+                    at[j] = -1;
                     if (x >= end) continue;
                     unsigned int token, head, piece;
+                    if (p.run != 0) {
+                        head = x / of_head;
+                        piece = (x - head * of_head) * sizeof(Piece);
+                        const long long off = head * p.head_stride + piece;
+                        if (piece + sizeof(Piece) > run) {
+                            for (; piece < run; piece += 4)
+                                *reinterpret_cast<uint32_t*>(to + head * p.head_stride + piece) =
+                                    *reinterpret_cast<const uint32_t*>(from + head * p.head_stride + piece);
+                            continue;
+                        }
+                        at[j] = off;
+                        v[j] = *reinterpret_cast<const Piece*>(from + off);
+                        continue;
+                    }
                     if (p.head_first) {
                         head = x / of_head;
                         piece = x - head * of_head;
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int j = 0; j < kCopyFly; ++j)
-                    if (k + j * kCopyThreads < end) *reinterpret_cast<Piece*>(to + at[j]) = v[j];
+                    if (at[j] >= 0) *reinterpret_cast<Piece*>(to + at[j]) = v[j];
             }
         }
     }
