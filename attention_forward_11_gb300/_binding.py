@@ -619,10 +619,14 @@ def _paged_fork(torch, handle, parents, kv_lens, free_pages, block_table, page_s
                 counts):
     i32, n = torch.int32, parents.numel()
     n_free, n_pages = free_pages.numel(), shares.numel()
-    _check_ints("parents", parents, i32, n)
-    _check_ints("kv_lens", kv_lens, i32, n)
-    _check_ints("free_pages", free_pages, i32, n_free)
-    _check_ints("shares", shares, i32, n_pages)
+    if not (parents.dtype is i32 and kv_lens.dtype is i32 and free_pages.dtype is i32 and shares.dtype is i32 and
+            parents.dim() == 1 and kv_lens.dim() == 1 and free_pages.dim() == 1 and shares.dim() == 1 and
+            kv_lens.numel() == n and parents.is_contiguous() and kv_lens.is_contiguous() and free_pages.is_contiguous() and
+            shares.is_contiguous()):
+        _check_ints("parents", parents, i32, n)
+        _check_ints("kv_lens", kv_lens, i32, n)
+        _check_ints("free_pages", free_pages, i32, n_free)
+        _check_ints("shares", shares, i32, n_pages)
     if lens is not None:
         _check_ints("lens", lens, i32, n)
     if free_head is not None:
@@ -668,11 +672,15 @@ def attn_paged_free(kv_lens, keep_lens, block_table, page_size: int, shares, fre
 def _paged_free(torch, handle, kv_lens, keep_lens, block_table, page_size, shares, free_pages, free_head, counts):
     i32, n = torch.int32, kv_lens.numel()
     n_free, n_pages = free_pages.numel(), shares.numel()
-    _check_ints("kv_lens", kv_lens, i32, n)
-    _check_ints("keep_lens", keep_lens, i32, n)
-    _check_ints("shares", shares, i32, n_pages)
-    _check_ints("free_pages", free_pages, i32, n_free)
-    _check_ints("free_head", free_head, i32, 1)
+    if not (kv_lens.dtype is i32 and keep_lens.dtype is i32 and shares.dtype is i32 and free_pages.dtype is i32 and
+            free_head.dtype is i32 and kv_lens.dim() == 1 and keep_lens.dim() == 1 and shares.dim() == 1 and
+            free_pages.dim() == 1 and free_head.dim() == 1 and keep_lens.numel() == n and free_head.numel() == 1 and
+            kv_lens.is_contiguous() and keep_lens.is_contiguous() and shares.is_contiguous() and free_pages.is_contiguous()):
+        _check_ints("kv_lens", kv_lens, i32, n)
+        _check_ints("keep_lens", keep_lens, i32, n)
+        _check_ints("shares", shares, i32, n_pages)
+        _check_ints("free_pages", free_pages, i32, n_free)
+        _check_ints("free_head", free_head, i32, 1)
     max_pages, table_stride = _table_shape(block_table, n, i32)
     if counts is None:
         counts = torch.empty(4, dtype=i32, device=kv_lens.device)
@@ -823,8 +831,10 @@ def _paged4_fwd(torch, handle, q, k_codes, k_scales, v_codes, v_scales, block_ta
         _bad("q", "bf16 or float16")
     n_pages, page_size, Hkv, D, strides = _cache4_shape(torch, k_codes, k_scales, v_codes, v_scales)
     n = kv_lens.numel()
-    _check_ints("kv_lens", kv_lens, i32, n)
-    _check_ints("cu_q", cu_q, i32, n + 1)
+    if not (kv_lens.dtype is i32 and cu_q.dtype is i32 and kv_lens.dim() == 1 and cu_q.dim() == 1 and
+            cu_q.numel() == n + 1 and kv_lens.is_contiguous() and cu_q.is_contiguous()):
+        _check_ints("kv_lens", kv_lens, i32, n)
+        _check_ints("cu_q", cu_q, i32, n + 1)
     if len(shape) != 3:
         _bad("q", "[T, Hq, D]")
     T, Hq, _ = shape

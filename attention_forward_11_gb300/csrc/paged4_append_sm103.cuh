@@ -11,7 +11,9 @@
 // A NaN or an infinity makes its block's scale 448 and is stored as +-6 (a NaN as +6).
 //
 // A thread has one block of K and the same block of V: 64 bytes read, 16 bytes of codes and
-// two bytes of scales written, four lanes' scales in one word.
+// two bytes of scales written, four lanes' scales in one word.  65000 rows of 16 heads of 64 take
+// 78 us, 4.4 TB/s of the bytes that are needed (0.64 of a copy's rate: scattered rows, 32 and 4
+// bytes at a place); 64 rows of 8 heads 2.3 us.
 #pragma once
 #include <cfloat>
 #include <cstdint>

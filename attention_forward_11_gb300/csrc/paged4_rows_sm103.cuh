@@ -3,19 +3,36 @@
 //
 // The kernel is paged_rows_sm103.cuh's: keys are the long side of the products m16n8k16, a warp
 // owns a slice of every tile with its own ring of cp.async copies and its own softmax state,
-// shares and pieces as in paged_sched_sm103.cuh.  With a quarter of the bytes a key, what
-// counts is the instructions between shared memory and the products, so no operand is put
-// together from its rows and columns: the products' sums run over any order of their terms, and
-// every lane takes the elements that lie together.
-//   S^T = K Q^T: lane (g, t) has the t-th quarter of the rows of keys g and g + 8, elements 4 j to
-//   4 j + 3 of it for product j, read as whole words; Q is loaded in the same order.
-//   O^T += V^T P^T: lane (g, t) has the g-th eighth of the rows of its four keys, and product j
-//   gives elements 2 j and 2 j + 1 of it.  A pair of the operand is one element of two keys, so
-//   two keys' nibbles are laid side by side (two instructions for four pairs) before they are
-//   converted.
-//   The scales of both are one or two a key and lane.
-// The keys' order within 16 (slot r is key perm(r)) and a swizzle of 16-byte pieces keep all
-// reads free of bank conflicts.
+// shares and pieces as in paged_sched_sm103.cuh.  A key has 0.28 of the bytes, so a call is bound
+// by its instructions: at HBM's rate a scheduler has 392 cycles for 16 keys of head size 128, and
+// the 64 conversions, 64 scalings (two cycles each, on ports that they share) and 16 products
+// alone take 256.  What is left is kept small:
+//   - No operand is put together from its rows and columns: the products' sums run over any order
+//     of their terms, and every lane takes the elements that lie together.
+//     S^T = K Q^T: lane (g, t) has the t-th quarter of the rows of keys g and g + 8, elements 4 j to
+//     4 j + 3 of it for product j, read as whole words; Q is loaded in the same order.
+//     O^T += V^T P^T: lane (g, t) has the g-th eighth of the rows of its four keys, and product j
+//     gives elements 2 j and 2 j + 1 of it.  A pair of the operand is one element of two keys, so
+//     two keys' nibbles are laid side by side (two instructions for four pairs) before they are
+//     converted.  The scales of both are one or two a key and lane.
+//   - The maximum that weights are relative to rises only when a logit is past it by 2^8 (164 to
+//     154 us for 144 sequences of 300 to 8000 keys, 64/8 heads of 128).
+//   - Where there are many units, a block is four teams of four warps, each with a share of its
+//     own: a unit's start and end are four warps' work, not sixteen's (198 to 164 us).  That takes
+//     128 registers a thread, so the share and both positions in it live in shared memory.
+//   - A unit's own cost is reckoned as 512 or 1024 keys (256 in the 16-bit kernel): 223 to 208 us.
+// The keys' order within 16 (slot r is key perm(r)) and a swizzle of 16-byte pieces keep all reads
+// free of bank conflicts.  L2 is asked for no more than a row of codes, since the next 64 bytes
+// belong to another head where pages are stored token by token (280 to 203 us).
+//
+// 144 sequences as above take 152 us, 4.8 TB/s of cache (203 stored token by token; the 16-bit
+// kernel 1.75 times as long on 48 of them); 8 of 32768 keys, one key head, 20 us (29 in 16 bits);
+// one of 1000 keys, 8 heads, 11 us (10), a block's start and end.  Bulk copies of 1 KB in place of
+// cp.async took 175 us, slices of 16 keys 189.
+//
+// P is rounded to fp16 for its product whatever q's type, which the products' operands are too:
+// against 64 bits O is off by 1.7e-3 of its norm in bf16 and 2.6e-4 in fp16, of which O's own rounding is
+// 1.65e-3 and 2.1e-4.
 #pragma once
 #include <cmath>
 #include <cstdint>

@@ -5,16 +5,25 @@
 // K/V tile, S, P and O in tensor memory, a softmax warpgroup per tile, work items posted by a
 // warp that walks the block's share.  All operands are fp16 (paged4_common_sm103.cuh).  What the
 // codes change:
-//   - The epilogue's warpgroup fills the stages instead of TMA: a row's codes are read by D / 32
-//     lanes straight into registers, a tile ahead, converted without rounding and stored where
-//     TMA would have put them.  A step's 32 K elements take about 1000 of its 2640 cycles, on
-//     warps that are idle between two epilogues otherwise.
+//   - The epilogue's warpgroup fills the stages instead of TMA: a row's codes are copied by D / 32
+//     lanes, each for itself and a tile ahead, converted without rounding and stored where TMA
+//     would have put them.
 //   - Every lane finds the page of a row of its own, so pages of any size are taken; rows without
 //     a key become zeros, so V needs no clean-up.
 //   - The softmax warps turn bf16 queries into fp16 in shared memory before their first product; a
-//     row's power of two goes into its softmax scale.
+//     row's power of two goes into its softmax scale.  (Between two fills it cost two prompts of
+//     8192, 32/8 heads, 890 instead of 808 us.)
 //   - Fills and epilogues are one sequence in a fixed order in which nothing waits for what comes
 //     behind it: item j's epilogue runs after the fill of the stage behind the one with its last V.
+//     It stores O as it comes out of tensor memory, a row's 64 bytes a thread.
+//
+// 512 tokens on 32256 cached ones, 64/8 heads of 128, take 428 us, 1275 TFLOP/s (the 16-bit kernel 337);
+// at head size 64 286 (252); two prompts of 8192, 32/8 heads, 808 us (630); 4 chunks of 100 to 512 among 36
+// tokens 165 us (171).  What bounds it is the fills' warpgroup, 2750 busy cycles a step of two row
+// tiles (1150 of conversions and stores, 1175 of page numbers, addresses and copies), and shared memory,
+// which the products read at its full rate half of the time.  Measured and not kept: codes by TMA into
+// shared staging (614 us); copies or addresses by other warps of the MMA's warpgroup, which slow its
+// issue (466 to 564); codes taken into registers before the stage is free (452).
 //
 // Waits are bounded as in the dense forward: after a timeout all roles leave, copies and
 // MMAs in flight are waited for, and tensor memory is freed.

@@ -423,6 +423,7 @@ attn_status_t attn_paged_copy(const int* copies, int n_copies, void* const* cach
  * rounded to the nearest e2m1, ties to the even code, 6 at most, with y's sign (product and quotients
  * in fp32).  Of a block with a NaN or an infinity the scale is 448, and those are stored as +-6 (a NaN
  * as +6).  Units are positive and finite, and so is 1 / unit in fp32.
+ * If two rows name one slot, it holds bytes of either afterwards, codes and scales apart.
  *
  * Errors and the rest as attn_paged_append.
  */

@@ -191,6 +191,28 @@ def test_fwd_long_caches(lens, Hq, Hkv, D):
     check(b, *run_fwd(b))
 
 
+@pytest.mark.parametrize("D,dtype,page,layout", [(64, HF, 16, "heads"), (64, BF, 7, "tokens"), (128, BF, 64, "heads"),
+                                                 (128, HF, 24, "turns"), (128, BF, 16, "tokens")])
+def test_fwd_more_units_than_blocks(D, dtype, page, layout):
+    """Batches whose units are shared out over teams of a block's warps: units of one tile, of many, cut by
+    several teams and by several blocks, places without rows, and the same bits whatever the workspace held."""
+    rng = random.Random(D + page)
+    lens = [(rng.choice([1, 2, 31, 130, 700]), 1) for _ in range(330)]
+    lens[7], lens[200], lens[329] = (30000, 1), (5000, 1), (9000, 1)
+    lens[50] = lens[51] = (0, 0)
+    b = Batch4(lens, 2, 1, D, page, dtype, layout=layout, pad_rows=2, seed=D)
+    ws = torch.full((fa.attn_paged_coded_fwd_workspace_size(b.T, 1, 2, 1, D, page),), 255, dtype=torch.uint8, device="cuda")
+    first = run_fwd(b, workspace=ws)
+    check(b, *first, untouched=9.0)
+    for _ in range(3):
+        again = run_fwd(b, workspace=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    b = Batch4([(257, 1)] * 160, 8, 2, D, page, dtype, layout=layout, seed=1)
+    check(b, *run_fwd(b))
+    b = Batch4([(64, 3)] * 200, 4, 2, D, page, dtype, layout=layout, seed=2)  # six rows a head
+    check(b, *run_fwd(b))
+
+
 def test_fwd_one_long_sequence_among_many():
     b = Batch4([(30000, 1)] + [(x, 1) for x in range(1, 200)], 4, 1, 64, 16, seed=3)
     check(b, *run_fwd(b))
