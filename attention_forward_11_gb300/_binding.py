@@ -706,19 +706,24 @@ def attn_paged_copy(copies, caches, stream=None) -> None:
     caches = list(caches)
     if not caches:
         _bad("caches", "at least one tensor")
-    device = _on_one_gpu(copies, *caches)
+    T = torch.Tensor  # a model has some hundred caches: each property is read by one map over them
+    devices = {copies.get_device(), *map(T.get_device, caches)}
+    device = devices.pop()
+    if devices or device < 0:
+        device = _on_one_gpu(copies, *caches)
     if copies.dtype is not torch.int32 or copies.dim() != 2 or copies.shape[1] != 3 or not copies.is_contiguous():
         _bad("copies", "a contiguous int32 [n, 3] tensor")
-    layouts = {}
-    for c in caches:
-        layouts.setdefault((c.shape, c.stride(), c.dtype), []).append(c.data_ptr())
+    ptrs = list(map(T.data_ptr, caches))
+    layouts = list(zip(map(T.stride, caches), map(T.size, caches), map(T.element_size, caches)))
     calls = []
-    n_pages, page_size = caches[0].shape[:2] if caches[0].dim() == 4 else (0, 0)
-    for (shape, stride, dtype), ptrs in layouts.items():
+    n_pages, page_size = layouts[0][1][:2] if len(layouts[0][1]) == 4 else (0, 0)
+    different = dict.fromkeys(layouts)
+    for layout in different:
+        stride, shape, size = layout
         if len(shape) != 4 or shape[0] != n_pages or shape[1] != page_size or (stride[3] != 1 and shape[3] > 1):
             _bad("caches", "[n_pages, page_size, heads, x] of one number and size of pages, the last axis contiguous")
-        size = dtype.itemsize
-        calls.append((copies.data_ptr(), copies.shape[0], (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), n_pages, page_size,
+        mine = ptrs if len(different) == 1 else [p for p, k in zip(ptrs, layouts) if k == layout]
+        calls.append((copies.data_ptr(), copies.shape[0], (ctypes.c_void_p * len(mine))(*mine), len(mine), n_pages, page_size,
                       shape[2], shape[3] * size, *(x * size for x in stride[:3])))
     if stream is None and torch._C._cuda_getDevice() == device:
         _paged_copy(calls, torch._C._cuda_getCurrentRawStream(device))

@@ -20,6 +20,12 @@ struct Cache4 {
 
 bool unit_ok(float unit) { return std::isfinite(unit) && unit > 0.f && std::isfinite(1.f / unit); }
 
+// Is a unit a power of two whose product with any scale's inverse is a normal number?
+bool short_unit(float inv) {
+    int e;
+    return std::frexp(inv, &e) == 0.5f && e >= -100 && e <= 100;
+}
+
 attn_status_t check_cache4(Cache4& c) {
     if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales) return ATTN_ERR_INVALID_ARG;
     if (c.n_pages < 1 || c.page_size < 1 || c.Hkv < 1 || c.D < 1) return ATTN_ERR_INVALID_ARG;
@@ -206,9 +212,10 @@ extern "C" attn_status_t attn_paged_coded_append(const void* k, const void* v, c
     p.by_page = attn::paged::make_fastdiv(static_cast<unsigned int>(page_size));
     p.by_row = attn::paged::make_fastdiv(static_cast<unsigned int>(p.row_blocks));
     const dim3 blocks(static_cast<unsigned int>(((long long)n_tokens + p.per_block - 1) / p.per_block));
-    return dtype == ATTN_DTYPE_F16
-               ? launch_behind(attn::paged::paged4_append_kernel<true>, blocks, attn::paged::kAppend4Threads, 0, stream, p)
-               : launch_behind(attn::paged::paged4_append_kernel<false>, blocks, attn::paged::kAppend4Threads, 0, stream, p);
+    const bool f16 = dtype == ATTN_DTYPE_F16, brief = short_unit(p.k_inv) && short_unit(p.v_inv);
+    auto kernel = f16 ? brief ? attn::paged::paged4_append_kernel<true, true> : attn::paged::paged4_append_kernel<true, false>
+                      : brief ? attn::paged::paged4_append_kernel<false, true> : attn::paged::paged4_append_kernel<false, false>;
+    return launch_behind(kernel, blocks, attn::paged::kAppend4Threads, 0, stream, p);
 }
 
 extern "C" attn_status_t attn_paged_coded_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,

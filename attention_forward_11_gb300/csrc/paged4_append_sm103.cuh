@@ -7,13 +7,16 @@
 // quotient that cvt rounds is y r (r = 1 / s) corrected by its remainder, y r + (y - (y r) s) r
 // with two fused products, which is within half a unit of its last place of y / s and equal to
 // it where y / s has few bits, as every border between two codes has (without the correction
-// 11 of the 56 pairs of a significand and a border fall on the wrong side).
+// 11 of the 56 pairs of a significand and a border fall on the wrong side).  Where the unit is a
+// power of two, y has as few bits as x: a quotient that is no border is at least 2^-12 of itself
+// away from one, the products y r that miss a border are one last place above it, and
+// clearing the product's last 8 bits puts both right (kShort: 3 instructions an element, not 6).
 // A NaN or an infinity makes its block's scale 448 and is stored as +-6 (a NaN as +6).
 //
 // A thread has one block of K and the same block of V: 64 bytes read, 16 bytes of codes and
-// two bytes of scales written, four lanes' scales in one word.  65000 rows of 16 heads of 64 take
-// 78 us, 4.4 TB/s of the bytes that are needed (0.64 of a copy's rate: scattered rows, 32 and 4
-// bytes at a place); 64 rows of 8 heads 2.3 us.
+// two bytes of scales written, four lanes' scales in one word.  Instruction issue bounds it, 70 % of
+// the slots at 53 % of DRAM's cycles: 65000 rows of 16 heads of 64 take 74 us on pages stored head
+// by head (78 without kShort), 64 token by token (5.35 TB/s); 64 rows of 8 heads 2.1 us.
 #pragma once
 #include <cfloat>
 #include <cstdint>
@@ -45,7 +48,7 @@ struct Coded {
     uint32_t scale;   // e4m3
 };
 
-template <bool kF16>
+template <bool kF16, bool kShort>
 __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float inv) {
     const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     // the bits of |x| are ordered like |x|, NaN above infinity
@@ -63,8 +66,10 @@ __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float 
             y[2 * i] = __uint_as_float(x[i] << 16);
             y[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
         }
-        y[2 * i] *= inv;
-        y[2 * i + 1] *= inv;
+        if constexpr (!kShort) {
+            y[2 * i] *= inv;
+            y[2 * i + 1] *= inv;
+        }
     }
     float top;
     if constexpr (kF16) asm("{.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.f32.f16 %0, l;}" : "=f"(top) : "r"(top_bits));
@@ -73,7 +78,7 @@ __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float 
     if (!(top <= FLT_MAX)) {  // a NaN, an infinity, or a unit too small for the row
         top = FLT_MAX;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = fmaxf(fminf(y[i], FLT_MAX), -FLT_MAX);
+        for (int i = 0; i < 16; ++i) y[i] = fmaxf(fminf(y[i], FLT_MAX), -FLT_MAX);  // kShort: of x, whose quotients saturate
     }
     Coded c;
     uint16_t two;
@@ -85,10 +90,16 @@ __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float 
     float s;
     asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;}" : "=f"(s) : "r"(s2));
     const float r = c.scale == 0 ? 0.f : __frcp_rn(s);
+    if constexpr (kShort) {
+        const float by = r * inv;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float t = y[i] * r;
-        y[i] = copysignf(fmaf(fmaf(-t, s, y[i]), r, t), y[i]);
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(__float_as_uint(y[i] * by) & 0xffffff00u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float t = y[i] * r;
+            y[i] = copysignf(fmaf(fmaf(-t, s, y[i]), r, t), y[i]);
+        }
     }
     uint32_t w[2];
 #pragma unroll
@@ -105,7 +116,8 @@ __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float 
     return c;
 }
 
-template <bool kF16>
+// kShort: both units are powers of two (and 2^100 at most, or one part in it).
+template <bool kF16, bool kShort>
 __global__ void __launch_bounds__(kAppend4Threads) paged4_append_kernel(const Append4Params p) {
     launch_dependents();
     wait_for_primary();
@@ -122,7 +134,7 @@ __global__ void __launch_bounds__(kAppend4Threads) paged4_append_kernel(const Ap
             const uint4* v = reinterpret_cast<const uint4*>(p.v + (row0 + r) * p.v_stride + b * 16ll);
             x[0] = k[0], x[1] = k[1], x[2] = v[0], x[3] = v[1];
         }
-        const Coded ck = encode16<kF16>(x[0], x[1], p.k_inv), cv = encode16<kF16>(x[2], x[3], p.v_inv);
+        const Coded ck = encode16<kF16, kShort>(x[0], x[1], p.k_inv), cv = encode16<kF16, kShort>(x[2], x[3], p.v_inv);
         uint32_t sk = ck.scale << (8 * (b & 3)), sv = cv.scale << (8 * (b & 3));
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
