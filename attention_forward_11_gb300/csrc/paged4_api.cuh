@@ -40,10 +40,13 @@ attn_status_t check_cache4(Cache4& c) {
                ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-template <int kD, int kNB, bool kMany = false>
+template <int kD, int kNB>
 bool opt_in_smem_rows4() {
-    return cudaFuncSetAttribute(attn::paged::paged4_rows_kernel<kD, kNB, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                attn::paged::Rows4Geo<kD, kNB, kMany>::kSmemBytes) == cudaSuccess;
+    using namespace attn::paged;
+    return cudaFuncSetAttribute(paged4_rows_kernel<kD, kNB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Rows4Geo<kD, kNB, false>::kSmemBytes) == cudaSuccess &&
+           cudaFuncSetAttribute(paged4_rows_kernel<kD, kNB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Rows4Geo<kD, kNB, true>::kSmemBytes) == cudaSuccess;
 }
 
 template <bool kF16, int kD>
@@ -62,7 +65,7 @@ bool paged4_device_setup(int dev, int* sm_count) {
         done[dev] = opt_in_smem_rows4<64, 1>() && opt_in_smem_rows4<64, 2>() && opt_in_smem_rows4<64, 3>() &&
                     opt_in_smem_rows4<64, 4>() && opt_in_smem_rows4<128, 1>() && opt_in_smem_rows4<128, 2>() &&
                     opt_in_smem_rows4<128, 3>() && opt_in_smem_rows4<256, 1>() && opt_in_smem_rows4<256, 2>() &&
-                    opt_in_smem_rows4<64, 1, true>() && opt_in_smem_rows4<128, 1, true>() && opt_in_smem_tiles4<false, 64>() &&
+                    opt_in_smem_tiles4<false, 64>() &&
                     opt_in_smem_tiles4<true, 64>() && opt_in_smem_tiles4<false, 128>() && opt_in_smem_tiles4<true, 128>();
     return done[dev];
 }
@@ -81,9 +84,12 @@ attn_status_t launch_rows4(const attn::paged::Paged4Params& p, void* workspace, 
 // Teams of four warps (paged4_rows_sm103.cuh) pay where most of them find work of their own, as far
 // as the host knows.  300 to 8000 keys, 64/8 heads of 128, sequences x heads with a place / with rows,
 // teams / whole blocks: 192 / 64 19.4 / 17.0 us, 320 / 192 33.5 / 38.4, 480 / 352 52.6 / 64.0, 672 /
-// 544 78.5 / 98.6, 1280 / 1152 152 / 198; 8 x 1 of 32767 keys 31.6 / 20.0.
-bool many_units(int total_q, int n_seqs, int Hkv, int sms) {
-    return (long long)std::min(total_q, n_seqs) * Hkv >= 2ll * sms;
+// 544 78.5 / 98.6, 1280 / 1152 152 / 198; 8 x 1 of 32767 keys 31.6 / 20.0.  More than 8 rows at head
+// size 64, 2000 to 6000 keys, 32 units 18.8 / 18.6, 128 38.0 / 39.5, 512 103 / 109; at 128 128 units 57.5 /
+// 55.3, 512 144 / 152; at 256 384 units 119 / 135.
+bool many_units(const attn::paged::Paged4Params& p, int nb, int D, int sms) {
+    const long long units = (long long)std::min(p.total_q, p.n_seqs) * p.Hkv;
+    return units >= (D == 64 && nb > 1 ? sms / 2 : 2 * sms);
 }
 
 // Does a call take the tcgen05 kernel?  From more rows a key/value head on than the rows kernel
@@ -93,21 +99,24 @@ bool takes_tiles4(long long rows, int D) { return rows > 8 * max_row_blocks(D) &
 size_t paged4_workspace_bytes(int sms, long long rows, int D) {
     if (takes_tiles4(rows, D)) return attn::paged::ws_bytes(sms, attn::kTiles * attn::kBM, D);
     const int nb = row_blocks_for(rows, D);
-    return attn::paged::ws_bytes(nb == 1 && D <= 128 ? 4 * sms : sms, 8 * nb, D);
+    return attn::paged::ws_bytes((nb == 1 && D <= 128 ? 4 : 2) * sms, 8 * nb, D);
 }
 
 // The rows kernel's variant for sequences of at most `rows` rows.
+template <int kD, bool kMany>
+attn_status_t launch_rows4_blocks(const attn::paged::Paged4Params& p, int nb, void* workspace, int sms, cudaStream_t stream) {
+    if (nb == 1) return launch_rows4<kD, 1, kMany>(p, workspace, sms, stream);
+    if constexpr (kD != 256)
+        if (nb == 3) return launch_rows4<kD, 3, kMany>(p, workspace, sms, stream);
+    if constexpr (kD == 64)
+        if (nb == 4) return launch_rows4<kD, 4, kMany>(p, workspace, sms, stream);
+    return launch_rows4<kD, 2, kMany>(p, workspace, sms, stream);
+}
 template <int kD>
 attn_status_t launch_rows4_for(const attn::paged::Paged4Params& p, long long rows, void* workspace, int sms, cudaStream_t stream) {
     const int nb = row_blocks_for(rows, kD);
-    if constexpr (kD != 256)
-        if (nb == 1 && many_units(p.total_q, p.n_seqs, p.Hkv, sms)) return launch_rows4<kD, 1, true>(p, workspace, sms, stream);
-    if (nb == 1) return launch_rows4<kD, 1>(p, workspace, sms, stream);
-    if constexpr (kD != 256)
-        if (nb == 3) return launch_rows4<kD, 3>(p, workspace, sms, stream);
-    if constexpr (kD == 64)
-        if (nb == 4) return launch_rows4<kD, 4>(p, workspace, sms, stream);
-    return launch_rows4<kD, 2>(p, workspace, sms, stream);
+    return many_units(p, nb, kD, sms) ? launch_rows4_blocks<kD, true>(p, nb, workspace, sms, stream)
+                                      : launch_rows4_blocks<kD, false>(p, nb, workspace, sms, stream);
 }
 
 template <bool kF16, int kD>

@@ -17,9 +17,11 @@
 //     converted.  The scales of both are one or two a key and lane.
 //   - The maximum that weights are relative to rises only when a logit is past it by 2^8 (164 to
 //     154 us for 144 sequences of 300 to 8000 keys, 64/8 heads of 128).
-//   - Where there are many units, a block is four teams of four warps, each with a share of its
-//     own: a unit's start and end are four warps' work, not sixteen's (198 to 164 us).  That takes
-//     128 registers a thread, so the share and both positions in it live in shared memory.
+//   - Where there are many units, a block is teams of four warps, each with a share of its own: a
+//     unit's start and end are four warps' work, not all of them's.  Up to 8 rows at head sizes 64
+//     and 128 there are four teams (198 to 164 us), which leaves 128 registers a thread, so the share
+//     and both positions in it live in shared memory; otherwise two (48 sequences at head size 256
+//     135 to 119 us, 64 times 5 drafted tokens of 4 heads at 128 152 to 144).
 //   - A unit's own cost is reckoned as 512 or 1024 keys (256 in the 16-bit kernel): 223 to 208 us.
 // The keys' order within 16 (slot r is key perm(r)) and a swizzle of 16-byte pieces keep all reads
 // free of bank conflicts.  L2 is asked for no more than a row of codes, since the next 64 bytes
@@ -84,8 +86,9 @@ constexpr float kRise = 8.f;  // log2 units
 
 template <int kD, int kNB, bool kMany>
 struct Rows4Geo {
-    static constexpr int kWarps = kMany ? 16 : 8;
-    static constexpr int kTeams = kMany ? 4 : 1;                           // of a block, each with a share of its own
+    // kMany: teams of four warps, as many as the registers allow
+    static constexpr int kWarps = kMany && kNB == 1 && kD <= 128 ? 16 : 8;
+    static constexpr int kTeams = kMany ? kWarps / 4 : 1;  // of a block, each with a share of its own
     static constexpr int kTeamWarps = kWarps / kTeams;
     static constexpr int kThreads = 32 * kWarps, kTeamThreads = 32 * kTeamWarps;
     static constexpr int kRows = 8 * kNB;
@@ -97,7 +100,7 @@ struct Rows4Geo {
     // a stage: K codes, V codes, K scales, V scales
     static constexpr int kV = kCodeBytes, kScales = 2 * kCodeBytes, kVScales = kScales + kScaleBytes;
     static constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
-    static constexpr int kStages = kMany ? (kD == 64 ? 4 : 2) : kD == 64 ? 6 : 4;
+    static constexpr int kStages = kWarps == 16 ? (kD == 64 ? 4 : 2) : kD == 64 ? 6 : 4;
     static constexpr int kChunks = kCodeRow / 16;  // 16-byte pieces of a row
     static constexpr int kMergeCols = 64;
     static constexpr int kMergeStride = kMergeCols + 2;  // rows 2 t of a warp, and 2 t + 1, fall into different banks

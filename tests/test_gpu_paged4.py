@@ -213,6 +213,19 @@ def test_fwd_more_units_than_blocks(D, dtype, page, layout):
     check(b, *run_fwd(b))
 
 
+@pytest.mark.parametrize("D,rows", [(64, 3), (64, 5), (64, 7), (128, 3), (128, 5), (256, 1), (256, 3)])
+def test_fwd_more_units_than_blocks_of_many_rows(D, rows):
+    """As above with four heads a head, so up to four blocks of rows, and head size 256."""
+    rng = random.Random(D + rows)
+    lens = [(rng.choice([rows, 40, 150]), rows) for _ in range(330)]
+    lens[3], lens[100], lens[329] = (12000, rows), (0, 0), (3000, rows)
+    b = Batch4(lens, 4, 1, D, 16, HF if rows == 3 else BF, layout="heads", pad_rows=1, seed=D)
+    first = run_fwd(b)
+    check(b, *first, untouched=9.0)
+    again = run_fwd(b)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_fwd_one_long_sequence_among_many():
     b = Batch4([(30000, 1)] + [(x, 1) for x in range(1, 200)], 4, 1, 64, 16, seed=3)
     check(b, *run_fwd(b))
@@ -546,6 +559,6 @@ def test_a_server_that_forks_and_frees(D, page):
 
 
 def test_format_is_exact_in_fp16():
-    """Every code times every finite scale, as the kernels convert them: one key, a query that picks one element."""
+    """Every code times every finite scale is a number of fp16."""
     products = np.multiply.outer(E2M1, E4M3[:127]).ravel()
     assert (products.astype(np.float16).astype(np.float64) == products).all()
