@@ -16,6 +16,11 @@
 namespace attn {
 namespace paged {
 
+// A logit s becomes the exponent s * scale - m in one fused product, whose product is exact, while m is a product
+// that was rounded: off by up to half a step of m, in all of a row's weights alike.  From m of this size on
+// (2^22, steps of 0.5) that could take a weight out of fp16's range, so the product is rounded first, as m was.
+constexpr float kLargeMax = 4194304.f;
+
 struct Paged4Params : PagedParams {  // its strides are the codes', in bytes
     const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
     long long scale_page, scale_token, scale_head;  // bytes

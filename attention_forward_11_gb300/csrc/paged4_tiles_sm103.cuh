@@ -546,6 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_run = m_tile;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                float by = sl2;
+                if (__any_sync(0xffffffffu, fabsf(m_use) >= kLargeMax)) {
+                    by = 1.f;
+#pragma unroll
+                    for (int jj = 0; jj < kBN; ++jj) s[jj] = __float_as_uint(__uint_as_float(s[jj]) * sl2);
+                }
                 const bool need = (kt > 0) && (alpha != 1.f);
                 if (__any_sync(0xffffffffu, need)) {
 #pragma unroll 1
@@ -574,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 16; q += 2) {
                             const int e = 32 * c + 2 * q;
                             float a0, a1, b0, b1;
-                            ffma2_bc(a0, a1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), sl2, -m_use);
-                            ffma2_bc(b0, b1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), sl2, -m_use);
+                            ffma2_bc(a0, a1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), by, -m_use);
+                            ffma2_bc(b0, b1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), by, -m_use);
                             a0 = ex2_approx(a0);
                             a1 = ex2_approx(a1);
                             b0 = ex2_approx(b0);
