@@ -9,6 +9,7 @@
 // [2^14, 2^15), exactly but for elements below 2^-28 of that (off by at most 2^-39 of it), and
 // its logits are scaled back.
 #pragma once
+#include <cfloat>
 #include <cstdint>
 
 #include "paged_common_sm103.cuh"
@@ -58,6 +59,12 @@ __device__ __forceinline__ float row_factor(uint32_t top_bits, float& inverse) {
     const uint32_t field = min(268u - (top_bits >> 7), 253u);
     inverse = __uint_as_float((254u - field) << 23);
     return __uint_as_float(field << 23);
+}
+// The scale of such a row's logits: kept a normal number.  A row of zeros, or one whose scale lies below, has
+// products of at most 2^35 and so logits of (nearly) zero whatever its scale, but a scale of zero would make NaN
+// of a masked logit, and an infinite one of a product of zero.
+__device__ __forceinline__ float row_scale(float scale_log2, float inverse) {
+    return fminf(fmaxf(scale_log2 * inverse, FLT_MIN), FLT_MAX);
 }
 // two bf16 times a factor -> two fp16
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float factor) {

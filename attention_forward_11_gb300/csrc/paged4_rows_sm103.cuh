@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
                 all_see = min(all_see, lim[nb][e]);
                 m[nb][e] = -INFINITY;
                 l[nb][e] = 0.f;
-                sl2[nb][e] = p.scale_log2 * __shfl_sync(0xffffffffu, back[nb], (2 * t4 + e) * 4);
+                sl2[nb][e] = row_scale(p.scale_log2, __shfl_sync(0xffffffffu, back[nb], (2 * t4 + e) * 4));
             }
         }
 #pragma unroll

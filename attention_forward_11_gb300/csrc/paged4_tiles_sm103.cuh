@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float inverse;
                 const float factor = row_factor(max(top2 & 0xffffu, top2 >> 16), inverse);
-                sl2 = p.scale_log2 * inverse;
+                sl2 = row_scale(p.scale_log2, inverse);
 #pragma unroll
                 for (int q = 0; q < kD / 8; ++q)
                     *piece(q) = make_uint4(bf16x2_to_f16x2(x[q].x, factor), bf16x2_to_f16x2(x[q].y, factor),
