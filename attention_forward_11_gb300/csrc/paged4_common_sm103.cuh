@@ -17,9 +17,16 @@
 namespace attn {
 namespace paged {
 
+// Weights are 2^(exponent - m) for an m that is kMaxBelow below the row's maximum when it is set and is set anew
+// when the maximum is past it by more than kMaxAbove, so all are at most 2^15 and fp16 holds them.  Weights of the
+// keys far below the maximum are fp16's small numbers, of steps of 2^-24: 2^-31 of the largest, where an m at the
+// maximum itself would lose all that 10^6 keys at 2^-26 of it sum to, a 60th of O.
+constexpr float kMaxBelow = 7.f, kMaxAbove = 15.f;
+
 // A logit s becomes the exponent s * scale - m in one fused product, whose product is exact, while m is a product
 // that was rounded: off by up to half a step of m, in all of a row's weights alike.  From m of this size on
-// (2^22, steps of 0.5) that could take a weight out of fp16's range, so the product is rounded first, as m was.
+// (2^22, steps of 0.5) that could take a weight out of fp16's range, so the product is rounded first, as m was
+// (by __fmul_rn, which is never fused with what follows).
 constexpr float kLargeMax = 4194304.f;
 
 struct Paged4Params : PagedParams {  // its strides are the codes', in bytes

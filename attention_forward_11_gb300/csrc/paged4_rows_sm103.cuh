@@ -15,7 +15,7 @@
 //     gives elements 2 j and 2 j + 1 of it.  A pair of the operand is one element of two keys, so
 //     two keys' nibbles are laid side by side (two instructions for four pairs) before they are
 //     converted.  The scales of both are one or two a key and lane.
-//   - The maximum that weights are relative to rises only when a logit is past it by 2^8 (164 to
+//   - The maximum that weights are relative to rises only when a logit is past it (kMaxAbove; 164 to
 //     154 us for 144 sequences of 300 to 8000 keys, 64/8 heads of 128).
 //   - Where there are many units, a block is teams of four warps, each with a share of its own: a
 //     unit's start and end are four warps' work, not all of them's.  Up to 8 rows at head sizes 64
@@ -81,8 +81,6 @@ __device__ __forceinline__ void lds_x4(uint32_t* r, uint32_t at) {
 __device__ __forceinline__ void lds_x2(uint32_t* r, uint32_t at) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
 }
-
-constexpr float kRise = 8.f;  // log2 units
 
 template <int kD, int kNB, bool kMany>
 struct Rows4Geo {
@@ -417,24 +415,23 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
                 uint32_t pf[kNB][kKS][2];
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
-                    // element e of block b: slot g + 8 (e / 2), row 2 t4 + e % 2.  The maximum that weights
-                    // are relative to rises when a logit is past it by more than kRise: weights are at
-                    // most 2^kRise, and most slices only look.
+                    // element e of block b: slot g + 8 (e / 2), row 2 t4 + e % 2.  Most slices only look
+                    // whether the maximum has to rise.
                     float mx[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         mx[e] = fmaxf(sc[nb][0][e], sc[nb][0][2 + e]);
 #pragma unroll
                         for (int b = 1; b < kKS; ++b) mx[e] = fmaxf(mx[e], fmaxf(sc[nb][b][e], sc[nb][b][2 + e]));
-                        mx[e] *= sl2[nb][e];
+                        mx[e] = __fmul_rn(mx[e], sl2[nb][e]);
                     }
-                    if (__any_sync(0xffffffffu, mx[0] - m[nb][0] > kRise || mx[1] - m[nb][1] > kRise)) {
+                    if (__any_sync(0xffffffffu, mx[0] - m[nb][0] > kMaxAbove || mx[1] - m[nb][1] > kMaxAbove)) {
                         float al[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-                            const float mn = fmaxf(m[nb][e], mx[e]);
+                            const float mn = fmaxf(m[nb][e], mx[e] - kMaxBelow);
                             al[e] = ex2_approx(m[nb][e] - (mn == -INFINITY ? 0.f : mn));
                             m[nb][e] = mn;
                             l[nb][e] *= al[e];
@@ -455,8 +452,8 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
                             by = 1.f;
 #pragma unroll
                             for (int b = 0; b < kKS; ++b) {
-                                sc[nb][b][e] *= sl2[nb][e];
-                                sc[nb][b][2 + e] *= sl2[nb][e];
+                                sc[nb][b][e] = __fmul_rn(sc[nb][b][e], sl2[nb][e]);
+                                sc[nb][b][2 + e] = __fmul_rn(sc[nb][b][2 + e], sl2[nb][e]);
                             }
                         }
 #pragma unroll

@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(T::kBarQReady + t));
             }
-            float m_run = -INFINITY;  // running max (log2 units of scaled logits) used by the weights
+            float m_run = -INFINITY;  // what the weights are relative to (log2 units of scaled logits)
             float l_run = 0.f;        // running sum of weights
 
             for (int kt = 0; kt < nt; ++kt, ++sc, nvis -= kBN) {
@@ -537,20 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float tmax = fmaxf(fmax3(fmax3(mx[0], mx[1], last(0)), fmax3(mx[2], mx[3], last(1)),
                                                fmax3(mx[4], mx[5], last(2))),
                                          fmax3(fmax3(mx[6], mx[7], last(3)), fmax3(last(4), last(5), last(6)), last(7)));
-                const float m_tile = tmax * sl2;
+                const float m_tile = __fmul_rn(tmax, sl2);
 
-                // raise the running max only when the tile max exceeds it by more than 2^15
+                // the maximum rises only when the tile's is past it
                 float alpha = 1.f;
-                if (m_tile - m_run > kRescaleLog2) {
-                    alpha = ex2_approx(m_run - m_tile);
-                    m_run = m_tile;
+                if (m_tile - m_run > kMaxAbove) {
+                    alpha = ex2_approx(m_run - (m_tile - kMaxBelow));
+                    m_run = m_tile - kMaxBelow;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
                 float by = sl2;
                 if (__any_sync(0xffffffffu, fabsf(m_use) >= kLargeMax)) {
                     by = 1.f;
 #pragma unroll
-                    for (int jj = 0; jj < kBN; ++jj) s[jj] = __float_as_uint(__uint_as_float(s[jj]) * sl2);
+                    for (int jj = 0; jj < kBN; ++jj) s[jj] = __float_as_uint(__fmul_rn(__uint_as_float(s[jj]), sl2));
                 }
                 const bool need = (kt > 0) && (alpha != 1.f);
                 if (__any_sync(0xffffffffu, need)) {

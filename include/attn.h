@@ -442,9 +442,9 @@ attn_status_t attn_paged_coded_append(const void* k, const void* v, const long l
  * attn_paged_coded_fwd_workspace_size bytes).  scale * k_unit * log2(e) is positive and finite in fp32.
  *
  * Arithmetic: K and V become fp16 without rounding, and q in bf16 does but for elements below 2^-28 of its
- * row's largest, which are off by at most 2^-39 of that.  P is rounded to fp16, products and softmax
- * statistics are fp32, O is rounded to nearest even once.  What unseen rows of the cache hold (scales that
- * are NaN among them) has no influence.
+ * row's largest, which are off by at most 2^-39 of that.  P is rounded to fp16, weights below 2^-21 of their row's
+ * largest to 2^-32 of it.  Products and softmax statistics are fp32, O is rounded to nearest even once.  What unseen
+ * rows of the cache hold (scales that are NaN among them) has no influence.
  */
 attn_status_t attn_paged_coded_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
                                              size_t* bytes);
