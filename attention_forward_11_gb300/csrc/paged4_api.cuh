@@ -78,6 +78,7 @@ attn_status_t launch_rows4(const attn::paged::Paged4Params& p, void* workspace, 
     sp.map = make_row_map(p.Hkv, p.group, G::kRows, 1);
     sp.ws = split_workspace(workspace, sms * G::kTeams, G::kRows);
     sp.tag = next_tag();
+    sp.o_unit = p.v_unit;
     return launch_behind(paged4_rows_kernel<kD, kNB, kMany>, dim3(sms), G::kThreads, G::kSmemBytes, stream, p, sp);
 }
 
@@ -128,6 +129,7 @@ attn_status_t launch_tiles4(const attn::paged::Paged4Params& p, long long rows, 
     SchedParams sp{};
     sp.map = make_row_map(p.Hkv, p.group, attn::kBM, attn::kTiles);
     sp.ws = split_workspace(workspace, sms, T::kRows);
+    sp.o_unit = p.v_unit;
     TilesParams tp{};
     tp.tile_tokens = sp.map.tokens / attn::kTiles;
     tp.q_rows = sp.map.heads * tp.tile_tokens;

@@ -559,13 +559,15 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
                         a0 += v.x * f;
                         a1 += v.y * f;
                     }
-                    a0 *= p.v_unit;
-                    a1 *= p.v_unit;
                     if (whole) {
                         const float inv = L == 0.f ? 0.f : 1.f / L;
                         const long long tok = x.q0 + w.token;
+                        a0 *= inv;
+                        a1 *= inv;
+                        a0 *= p.v_unit;  // last: the sums times the unit may be no numbers of fp32
+                        a1 *= p.v_unit;
                         *reinterpret_cast<uint32_t*>(p.o + (tok * p.Hq + w.head) * kD + d) =
-                            p.f16 ? pack_x2<true>(a0 * inv, a1 * inv) : pack_x2<false>(a0 * inv, a1 * inv);
+                            p.f16 ? pack_x2<true>(a0, a1) : pack_x2<false>(a0, a1);
                         if (d == 0 && p.lse != nullptr)
                             p.lse[(long long)w.head * p.total_q + tok] =
                                 L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;

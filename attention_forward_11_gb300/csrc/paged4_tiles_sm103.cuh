@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // row of [total_q, Hq] (at most 2^31 - 1 of them); negative: no such row
                 const int out_row = there ? (w.q0 + token) * p.Hq + head : -1;
                 const uint32_t tO = tmem_base + lane_off + kTmemO + 128 * t;
-                const float inv_l = ml.y == 0.f ? 0.f : p.v_unit / ml.y;
+                const float inv_l = ml.y == 0.f ? 0.f : 1.f / ml.y;
                 const size_t ws_row = static_cast<size_t>(w.slot >= 0 ? w.slot : 0) * T::kRows + t * kBM + r;
                 // A thread stores its row's 32 columns as they come: whole sectors
 #pragma unroll
@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float4* dst = reinterpret_cast<float4*>(sp.ws.o + ws_row * kD + 32 * h);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(__uint_as_float(o[4 * q]) * p.v_unit, __uint_as_float(o[4 * q + 1]) * p.v_unit,
-                                                 __uint_as_float(o[4 * q + 2]) * p.v_unit, __uint_as_float(o[4 * q + 3]) * p.v_unit);
+                            dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                                 __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
                         continue;
                     }
                     uint4* dst = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(out_row) * kD + 32 * h);
@@ -676,9 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q) {
                         float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2)
+                        for (int e = 0; e < 8; e += 2) {
                             fmul2_b(f[e], f[e + 1], __uint_as_float(o[8 * q + e]), __uint_as_float(o[8 * q + e + 1]),
                                     inv_l);
+                            fmul2_b(f[e], f[e + 1], f[e], f[e + 1], p.v_unit);
+                        }
                         dst[q] = make_uint4(pack_x2<kF16>(f[0], f[1]), pack_x2<kF16>(f[2], f[3]),
                                             pack_x2<kF16>(f[4], f[5]), pack_x2<kF16>(f[6], f[7]));
                     }

@@ -115,10 +115,11 @@ struct RowsGeo {
 };
 
 // Joins the n pieces of a unit that block `first` started: M = max m, L = sum l 2^(m - M),
-// O = sum O 2^(m - M) / L.  kD / 4 threads have a row (four columns each), or, when there are
-// fewer rows than such groups, a part of a row's pieces; `buf` is shared scratch of a row and
-// its sum for every group.  `bar`: the threads are a team of their block with that barrier.  A block does this alone at its end, so what counts is how many
-// loads wait on one another: kFly pieces are in flight at once, the first before M is known.
+// O = sum O 2^(m - M) / L (times o_unit).  kD / 4 threads have a row (four columns each), or,
+// when there are fewer rows than such groups, a part of a row's pieces; `buf` is shared scratch of
+// a row and its sum for every group.  `bar`: the threads are a team of their block with that
+// barrier.  A block does this alone at its end, so what counts is how many loads wait on one
+// another: kFly pieces are in flight at once, the first before M is known.
 template <bool kF16, int kD, int kRows, int kThreads, int kFly = 20>
 __device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedParams& sp, const Seq& x, int head_unit, int t0,
                                             int first, int n, float* buf, int bar = 0) {
@@ -185,10 +186,10 @@ __device__ __forceinline__ void join_pieces(const PagedParams& p, const SchedPar
                 }
         }
         if (!mine || part != 0) continue;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? 0.f : 1.f / L, unit = sp.o_unit;
         const size_t tok = (size_t)x.q0 + w.token;
         *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
-            make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
+            make_uint2(pack_x2<kF16>(acc.x * inv * unit, acc.y * inv * unit), pack_x2<kF16>(acc.z * inv * unit, acc.w * inv * unit));
         if (col == 0 && p.lse != nullptr)
             p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }

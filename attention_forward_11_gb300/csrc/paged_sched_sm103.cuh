@@ -83,6 +83,8 @@ struct SchedParams {
     RowMap map;
     Workspace ws;
     unsigned long long tag;  // of this launch, 48 bits, not zero
+    float o_unit = 1.f;      // O is what the pieces give times this: last, since their sums times it may be no
+                             // numbers of fp32
 };
 
 // a / b for a, b >= 0; most fit 32 bits, where a division is several times cheaper
@@ -438,7 +440,7 @@ __device__ __forceinline__ bool count_piece(unsigned long long* word, int n) {
     return last;
 }
 
-// Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, the
+// Joins the pieces of cut units: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L (times o_unit), the
 // sums in the order of the pieces.  Grid (G, parts of a unit's rows): block (c, y) has a part of the
 // rows of the unit that block c of the first kernel starts, kD / 4 threads a row with four
 // columns each.  Most units have two or three pieces, so what the kernel costs is its
@@ -503,10 +505,10 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
             if (i0 >= h.n) break;
             load(i0);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? 0.f : 1.f / L, unit = sp.o_unit;
         const size_t tok = (size_t)x.q0 + w.token;
         *reinterpret_cast<uint2*>(p.o + (tok * p.Hq + w.head) * kD + col) =
-            make_uint2(pack_x2<kF16>(acc.x * inv, acc.y * inv), pack_x2<kF16>(acc.z * inv, acc.w * inv));
+            make_uint2(pack_x2<kF16>(acc.x * inv * unit, acc.y * inv * unit), pack_x2<kF16>(acc.z * inv * unit, acc.w * inv * unit));
         if (col == 0 && p.lse != nullptr)
             p.lse[(size_t)w.head * p.total_q + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }
