@@ -261,7 +261,7 @@ extern "C" attn_status_t attn_paged_coded_fwd(const void* q, const void* k_codes
     if (st != ATTN_OK) return st;
     if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
     const double scale_log2 = static_cast<double>(scale) * k_unit * 1.4426950408889634;
-    if (!std::isfinite(static_cast<float>(scale_log2)) || !(static_cast<float>(scale_log2) > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (!std::isnormal(static_cast<float>(scale_log2))) return ATTN_ERR_INVALID_ARG;  // fewer bits would move logits
     if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F16) return ATTN_ERR_INVALID_ARG;
     const long long row = (long long)Hq * D;
     if (q_stride % 8 != 0 || q_stride < row || q_stride > (1ll << 60) / total_q) return ATTN_ERR_INVALID_ARG;

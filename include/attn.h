@@ -439,7 +439,7 @@ attn_status_t attn_paged_coded_append(const void* k, const void* v, const long l
  * attn_paged_coded_fwd -- attn_paged_fwd over a cache in 4 bits.
  *
  * q, o and lse are bf16 or fp16 and fp32 as there, and so are all other arguments and the workspace (of
- * attn_paged_coded_fwd_workspace_size bytes).  scale * k_unit * log2(e) is positive and finite in fp32.
+ * attn_paged_coded_fwd_workspace_size bytes).  scale * k_unit * log2(e) is a normal number of fp32.
  *
  * Arithmetic: K and V become fp16 without rounding, and q in bf16 does but for elements below 2^-28 of its
  * row's largest, which are off by at most 2^-39 of that.  P is rounded to fp16, weights below 2^-21 of their row's
