@@ -658,7 +658,7 @@ def attn_paged_free(kv_lens, keep_lens, block_table, page_size: int, shares, fre
     [n_free], the list of attn_paged_tables, whose entries before free_head (int32 [1], read) have been
     taken: the freed pages become the entries in front of it, in ascending order.  Returns counts int32
     [4]: pages listed, next free_head, pages without room, rows cut inside a shared page; allocated
-    here if None.
+    here if None.  After a CUDA error (ATTN_ERR_CUDA) shares is undefined: the call is not repeated.
     """
     torch = _torch or _load_torch()
     device = _on_one_gpu(kv_lens, keep_lens, block_table, shares, free_pages, free_head, counts)

@@ -33,7 +33,9 @@ int row_tokens(int max_pages, int page_size) {
 }
 
 // Entries of a table from which on its rows are given to the whole GPU (1024 rows of 470 entries, all
-// freed, 26 us, in the one cluster 44; 300 rows 16 / 22 us; 128 rows 12.9 / 12.8 us).
+// freed, 26 us, in the one cluster 44; 300 rows 16 / 22 us; 128 rows 12.9 / 12.8 us; 256 rows of 256, or of
+// 1024, 13.8 / 14.2).  What is given back is on the device, so a wide table takes it for a few pages too: drafts
+// of 256 rows 9.2 us, in the one cluster 8.5.
 constexpr long long kFreeLarge = 65536;
 
 }  // namespace

@@ -16,8 +16,9 @@
 // rows gives a shared page its last push depends on timing, so the freed pages are listed by
 // number: the counts are lowered first, then every page whose count is below zero is found by
 // a scan over all counts.  Both halves are one launch of one cluster of 8 blocks, whose
-// hardware barrier stands between them; no workspace.  Where a table is large 8 SMs take longer
-// over its rows than a second launch does, and the first half is a launch over all of them.
+// hardware barrier stands between them; no workspace.  Where a table is large (kFreeLarge) 8 SMs
+// take longer over its rows than a second launch does, and the first half is a launch of its own
+// over all of them.
 //
 // Drafts of 256 rows given back take 8.7 us, 1024 rows of up to 470 pages 26 us.
 //

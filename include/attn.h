@@ -370,9 +370,11 @@ attn_status_t attn_paged_fork(const int* parents, const int* lens, int* kv_lens,
  *             rows cut inside a page that is still shared, which is not to be written to: fork the
  *             row instead.
  *
- * Asynchronous on `stream`, one kernel, no workspace; results do not depend on timing.  All
- * buffers are 4-byte aligned; no output overlaps an input or another output; every size is at
- * least 1.  On any error return nothing was launched.
+ * Asynchronous on `stream`, one kernel, or two where the table has 65536 entries (n_seqs * max_pages) or more; no
+ * workspace; results do not depend on timing.  All buffers are 4-byte aligned; no output overlaps an input or another
+ * output; every size is at least 1.  On any error return that is not ATTN_ERR_CUDA nothing was launched.  After
+ * ATTN_ERR_CUDA the first of two kernels may have lowered counts: shares is undefined then, and a second call would
+ * lower them again.
  */
 attn_status_t attn_paged_free(const int* kv_lens, const int* keep_lens, int n_seqs, int page_size,
                               const int* block_table, int max_pages, long long table_stride, int* shares,
