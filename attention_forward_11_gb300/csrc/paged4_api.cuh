@@ -20,9 +20,10 @@ struct Cache4 {
 
 bool unit_ok(float unit) { return std::isfinite(unit) && unit > 0.f && std::isfinite(1.f / unit); }
 
-// Is a unit a power of two whose product with any scale's inverse is a normal number?
+// Is the inverse of a unit a power of two, from 2^-101 to 2^99, whose product with any scale's inverse is a normal
+// number?
 bool short_unit(float inv) {
-    int e;
+    int e;  // inv is 2^(e - 1)
     return std::frexp(inv, &e) == 0.5f && e >= -100 && e <= 100;
 }
 

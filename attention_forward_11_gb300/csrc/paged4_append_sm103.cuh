@@ -116,7 +116,7 @@ __device__ __forceinline__ Coded encode16(const uint4& a, const uint4& b, float 
     return c;
 }
 
-// kShort: both units are powers of two (and 2^100 at most, or one part in it).
+// kShort: both units are powers of two, from 2^-99 to 2^101.
 template <bool kF16, bool kShort>
 __global__ void __launch_bounds__(kAppend4Threads) paged4_append_kernel(const Append4Params p) {
     launch_dependents();
