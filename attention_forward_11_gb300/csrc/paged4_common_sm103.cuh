@@ -23,11 +23,9 @@ namespace paged {
 // maximum itself would lose all that 10^6 keys at 2^-26 of it sum to, a 60th of O.
 constexpr float kMaxBelow = 7.f, kMaxAbove = 15.f;
 
-// A logit s becomes the exponent s * scale - m in one fused product, whose product is exact, while m is a product
-// that was rounded: off by up to half a step of m, in all of a row's weights alike.  From m of this size on
-// (2^22, steps of 0.5) that could take a weight out of fp16's range, so the product is rounded first, as m was
-// (by __fmul_rn, which is never fused with what follows).
-constexpr float kLargeMax = 4194304.f;
+// An exponent is one fused product, whose product is exact, less an m that was rounded: off by up to half a step of
+// m, in all of a row's weights alike.  Below 2^23 that is at most 1/2, and weights stay below fp16's 65504; the
+// entry point's contract ends there.
 
 struct Paged4Params : PagedParams {  // its strides are the codes', in bytes
     const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;

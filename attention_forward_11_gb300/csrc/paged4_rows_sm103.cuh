@@ -423,9 +423,9 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
                         mx[e] = fmaxf(sc[nb][0][e], sc[nb][0][2 + e]);
 #pragma unroll
                         for (int b = 1; b < kKS; ++b) mx[e] = fmaxf(mx[e], fmaxf(sc[nb][b][e], sc[nb][b][2 + e]));
-                        mx[e] = __fmul_rn(mx[e], sl2[nb][e]);
+                        mx[e] *= sl2[nb][e];
                     }
-                    if (__any_sync(0xffffffffu, mx[0] - m[nb][0] > kMaxAbove || mx[1] - m[nb][1] > kMaxAbove)) {
+                    if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + kMaxAbove || mx[1] > m[nb][1] + kMaxAbove)) {
                         float al[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -447,21 +447,12 @@ __global__ void __launch_bounds__(Rows4Geo<kD, kNB, kMany>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float use = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
-                        float by = sl2[nb][e];
-                        if (fabsf(use) >= kLargeMax) {
-                            by = 1.f;
-#pragma unroll
-                            for (int b = 0; b < kKS; ++b) {
-                                sc[nb][b][e] = __fmul_rn(sc[nb][b][e], sl2[nb][e]);
-                                sc[nb][b][2 + e] = __fmul_rn(sc[nb][b][2 + e], sl2[nb][e]);
-                            }
-                        }
 #pragma unroll
                         for (int b = 0; b < kKS; ++b)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 float& y = sc[nb][b][2 * u + e];
-                                y = ex2_approx(fmaf(y, by, -use));
+                                y = ex2_approx(fmaf(y, sl2[nb][e], -use));
                                 l[nb][e] += y;
                             }
                     }

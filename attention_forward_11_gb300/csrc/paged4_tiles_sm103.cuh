@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float tmax = fmaxf(fmax3(fmax3(mx[0], mx[1], last(0)), fmax3(mx[2], mx[3], last(1)),
                                                fmax3(mx[4], mx[5], last(2))),
                                          fmax3(fmax3(mx[6], mx[7], last(3)), fmax3(last(4), last(5), last(6)), last(7)));
-                const float m_tile = __fmul_rn(tmax, sl2);
+                const float m_tile = tmax * sl2;
 
                 // the maximum rises only when the tile's is past it
                 float alpha = 1.f;
@@ -546,12 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_run = m_tile - kMaxBelow;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                float by = sl2;
-                if (__any_sync(0xffffffffu, fabsf(m_use) >= kLargeMax)) {
-                    by = 1.f;
-#pragma unroll
-                    for (int jj = 0; jj < kBN; ++jj) s[jj] = __float_as_uint(__fmul_rn(__uint_as_float(s[jj]), sl2));
-                }
                 const bool need = (kt > 0) && (alpha != 1.f);
                 if (__any_sync(0xffffffffu, need)) {
 #pragma unroll 1
@@ -580,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 16; q += 2) {
                             const int e = 32 * c + 2 * q;
                             float a0, a1, b0, b1;
-                            ffma2_bc(a0, a1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), by, -m_use);
-                            ffma2_bc(b0, b1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), by, -m_use);
+                            ffma2_bc(a0, a1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), sl2, -m_use);
+                            ffma2_bc(b0, b1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), sl2, -m_use);
                             a0 = ex2_approx(a0);
                             a1 = ex2_approx(a1);
                             b0 = ex2_approx(b0);

@@ -442,6 +442,7 @@ attn_status_t attn_paged_coded_append(const void* k, const void* v, const long l
  *
  * q, o and lse are bf16 or fp16 and fp32 as there, and so are all other arguments and the workspace (of
  * attn_paged_coded_fwd_workspace_size bytes).  scale * k_unit * log2(e) is a normal number of fp32.
+ * Logits times log2(e) are below 2^23 in size: O and LSE of a row with larger ones may be NaN.
  *
  * Arithmetic: K and V become fp16 without rounding, and q in bf16 does but for elements below 2^-28 of its
  * row's largest, which are off by at most 2^-39 of that.  P is rounded to fp16, weights below 2^-21 of their row's

@@ -1,14 +1,12 @@
-"""Attention over the cache in 4 bits with logits so large that a step of fp32 between them is a factor of a weight:
-weights are relative to the row's own maximum and never past it."""
+"""Attention over the cache in 4 bits with the largest logits that the contract allows (2^23 in log2 units): the
+rounding of a row's maximum, half a step there, moves all of its weights alike and none out of fp16's range."""
 import numpy as np
 import pytest
 import torch
 
 import attention_forward_11_gb300 as fa
 from paged4_levels import Levels
-from paged4_ref import Batch4
-from paged_ref import check
-from test_gpu_paged4 import DECODE, MIXED, VERIFY, run_fwd
+from test_gpu_paged4 import run_fwd
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -21,7 +19,7 @@ def _built():
     fa.load_library()
 
 
-@pytest.mark.parametrize("gap", [3.0e5, 1.1 * 2.0 ** 22, 7.3 * 2.0 ** 25, 2.0 ** 30 / 3, 1.7 * 2.0 ** 45, 1.2 * 2.0 ** 100])
+@pytest.mark.parametrize("gap", [3.0e5, 1.1 * 2.0 ** 22, 2.0 ** 24 / 2.1])
 @pytest.mark.parametrize("q0", [1.0, -1.0])
 @pytest.mark.parametrize("lens", [[(4000, 1)], [(300, 1)] * 160, [(1000, 5)] * 3, [(3500, 130)], [(300, 1)] * 20 + [(700, 200)]],
                          ids=["one", "many", "verify", "chunk", "mixed"])
@@ -40,23 +38,3 @@ def test_two_sizes_of_logits_far_apart(lens, D, dtype, q0, gap):
         n = np.array([sum(high(j) == top for j in range(kv - x + t + 1)) for kv, x in lens for t in range(x)])
         exact = z + np.log(n)
         assert (np.abs(lse.double().cpu().numpy() - exact) <= 2.0 ** -21 * (1 + np.abs(exact)) + n * 2.0 ** -23).all()
-
-
-@pytest.mark.parametrize("scale", [2.0 ** 24, 2.0 ** 60])
-@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (256, BF), (128, HF)])
-@pytest.mark.parametrize("lens", [DECODE, VERIFY, MIXED], ids=["decode", "verify", "mixed"])
-def test_logits_of_many_sizes(lens, D, dtype, scale):
-    """Rows from fp16's smallest numbers on: O stays among the values of the keys that are seen."""
-    b = Batch4(lens, 4, 2, D, 16, dtype, pad_rows=1, seed=D)
-    b.scale = scale
-    b.q = (b.q.float() * 2.0 ** (-24 + 8.0 * (torch.arange(b.q.shape[0] * 4) % 4).reshape(-1, 4, 1))).to(dtype)
-    o, lse = run_fwd(b)
-    check(b, o, lse, untouched=9.0)
-    at = 0
-    for (kv, n), (_, v) in zip(lens, b.dense):
-        for t in range(n):
-            seen = np.repeat(np.asarray(v)[:kv - n + t + 1], 2, axis=1)
-            x = o[at + t].double().cpu().numpy()
-            step = 2.0 ** -7 * np.abs(seen).max(axis=0)
-            assert (x <= seen.max(axis=0) + step).all() and (x >= seen.min(axis=0) - step).all()
-        at += n

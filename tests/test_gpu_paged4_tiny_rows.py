@@ -20,8 +20,11 @@ def _built():
     fa.load_library()
 
 
-@pytest.mark.parametrize("scale,k_unit", [(2.0 ** -24, 1.0), (2.0 ** -30, 1.0), (0.088, 1e-7), (2.0 ** -120, 1.0), (2.0 ** 60, 1.0)])
-@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (256, BF), (128, HF)])
+SCALES = [(2.0 ** -24, 1.0), (2.0 ** -30, 1.0), (0.088, 1e-7), (2.0 ** -120, 1.0)]
+
+
+@pytest.mark.parametrize("D,dtype,scale,k_unit", [(D, t, *s) for D, t in ((64, BF), (128, BF), (256, BF), (128, HF)) for s in SCALES] +
+                         [(D, BF, 2.0 ** 60, 1.0) for D in (64, 128, 256)])  # with fp16's numbers past the largest logits
 @pytest.mark.parametrize("lens", [DECODE, VERIFY, MIXED], ids=["decode", "verify", "mixed"])
 def test_rows_of_zeros_and_of_tiny_numbers(lens, D, dtype, scale, k_unit):
     b = Batch4(lens, 4, 2, D, 16, dtype, k_unit=k_unit, pad_rows=1, seed=D)
