@@ -95,7 +95,7 @@ bool many_units(const attn::paged::Paged4Params& p, int nb, int D, int sms) {
 }
 
 // Does a call take the tcgen05 kernel?  From more rows a key/value head on than the rows kernel
-// computes together, on pages of any size.
+// computes together, on pages of any size (and unless V's unit is tiny: the rows kernel needs less workspace).
 bool takes_tiles4(long long rows, int D) { return rows > 8 * max_row_blocks(D) && D <= 128; }
 
 size_t paged4_workspace_bytes(int sms, long long rows, int D) {
@@ -150,7 +150,7 @@ template <int kD>
 attn_status_t launch_paged4(const attn::paged::Paged4Params& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
     const long long rows = (long long)max_q_len * p.group;
     if constexpr (kD != 256) {
-        if (takes_tiles4(rows, kD)) {
+        if (takes_tiles4(rows, kD) && p.v_unit >= attn::paged::kTiles4LeastUnit) {
             attn::paged::Paged4Params half = p;
             if (is_mixed(p, max_q_len, kD)) {
                 half.split_rows = 8 * row_blocks_for(p.group, kD);

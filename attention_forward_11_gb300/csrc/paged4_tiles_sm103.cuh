@@ -49,6 +49,10 @@ constexpr int kTiles4RegsSoftmax = 168, kTiles4RegsEpilogue = 112, kTiles4RegsOt
 static_assert(2 * kTiles4RegsSoftmax + kTiles4RegsEpilogue + kTiles4RegsOther <= 4 * (65536 / kThreads),
               "register split exceeds the launch allocation");
 
+// The smallest unit of V whose quotient by a row's sum, at most 2^47 (2^31 weights below 2^16), is a normal number:
+// the epilogue's one product for both costs two prompts of 8192 786 us, one for each 798.
+constexpr float kTiles4LeastUnit = 0x1p-79f;
+
 template <int kD>
 struct Tiles4Geo {
     static_assert(kD == 64 || kD == 128, "head size 64 or 128");
@@ -639,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // row of [total_q, Hq] (at most 2^31 - 1 of them); negative: no such row
                 const int out_row = there ? (w.q0 + token) * p.Hq + head : -1;
                 const uint32_t tO = tmem_base + lane_off + kTmemO + 128 * t;
-                const float inv_l = ml.y == 0.f ? 0.f : 1.f / ml.y;
+                const float inv_l = ml.y == 0.f ? 0.f : p.v_unit / ml.y;  // a normal number (kTiles4LeastUnit)
                 const size_t ws_row = static_cast<size_t>(w.slot >= 0 ? w.slot : 0) * T::kRows + t * kBM + r;
                 // A thread stores its row's 32 columns as they come: whole sectors
 #pragma unroll
@@ -670,11 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q) {
                         float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
+                        for (int e = 0; e < 8; e += 2)
                             fmul2_b(f[e], f[e + 1], __uint_as_float(o[8 * q + e]), __uint_as_float(o[8 * q + e + 1]),
                                     inv_l);
-                            fmul2_b(f[e], f[e + 1], f[e], f[e + 1], p.v_unit);
-                        }
                         dst[q] = make_uint4(pack_x2<kF16>(f[0], f[1]), pack_x2<kF16>(f[2], f[3]),
                                             pack_x2<kF16>(f[4], f[5]), pack_x2<kF16>(f[6], f[7]));
                     }
