@@ -817,7 +817,8 @@ def attn_paged_coded_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, c
 
     q, block_table, cu_q, kv_lens, max_q_len, causal, scale, o, lse, workspace and what is returned are as
     there (the workspace of attn_paged_coded_fwd_workspace_size bytes); the cache and its units as in
-    attn_paged_coded_append.
+    attn_paged_coded_append.  Logits times log2(e) are below 2^23 in size, and scale * k_unit * log2(e) is a
+    normal number of fp32.
     """
     torch = _torch or _load_torch()
     device = _on_one_gpu(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, o, lse, workspace)

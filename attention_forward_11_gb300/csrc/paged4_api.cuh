@@ -96,6 +96,8 @@ bool many_units(const attn::paged::Paged4Params& p, int nb, int D, int sms) {
 
 // Does a call take the tcgen05 kernel?  From more rows a key/value head on than the rows kernel
 // computes together, on pages of any size (and unless V's unit is tiny: the rows kernel needs less workspace).
+// 16 sequences of 2000 to 6000 keys, 8 key heads, rows / tiles kernel: at head size 128 16 rows 41 / 73 us, 24 54 / 71,
+// 32 83 / 69, 40 76 / 62, 64 111 / 66; at 64 24 34 / 55, 32 45 / 53, 40 54 / 48, 64 61 / 50.
 bool takes_tiles4(long long rows, int D) { return rows > 8 * max_row_blocks(D) && D <= 128; }
 
 size_t paged4_workspace_bytes(int sms, long long rows, int D) {
@@ -146,6 +148,12 @@ attn_status_t launch_tiles4(const attn::paged::Paged4Params& p, long long rows, 
                          stream, static_cast<const PagedParams&>(p), sp);
 }
 
+// Batches of long sequences and single tokens are shared by is_mixed, whose thresholds are the 16-bit kernels'.
+// Over codes the rows kernel is faster and a tile's step slower, so sharing wins sooner: one chunk among tokens,
+// 32/8 heads, longest / mean in brackets, all rows in tiles / shared: at head size 128, contexts of 100 to 1000 keys,
+// 34 / 34 us (17), 60 / 53 (36), 80 / 58 (50), 127 / 68 (84), 249 / 107 (156); of 2000 to 8000 119 / 95, 213 / 125,
+// 286 / 138, 451 / 195, 857 / 336; at 64 25 / 28, 43 / 41, 56 / 45, 84 / 52, 165 / 74, and 96 / 67, 158 / 96, 213 / 104,
+// 334 / 142, 635 / 251.  4 chunks of 100 to 512 among 36 tokens, 500 to 6000 keys, head size 128, 166 / 127 (20).
 template <int kD>
 attn_status_t launch_paged4(const attn::paged::Paged4Params& p, int max_q_len, void* workspace, int sms, cudaStream_t stream) {
     const long long rows = (long long)max_q_len * p.group;

@@ -14,9 +14,11 @@
 // A NaN or an infinity makes its block's scale 448 and is stored as +-6 (a NaN as +6).
 //
 // A thread has one block of K and the same block of V: 64 bytes read, 16 bytes of codes and
-// two bytes of scales written, four lanes' scales in one word.  Instruction issue bounds it, 70 % of
-// the slots at 53 % of DRAM's cycles: 65000 rows of 16 heads of 64 take 74 us on pages stored head
-// by head (78 without kShort), 64 token by token (5.35 TB/s); 64 rows of 8 heads 2.1 us.
+// two bytes of scales written, four lanes' scales in one word.  65000 rows of 16 heads of 64 in scattered
+// slots take 74 us on pages stored head by head (78 without kShort), 64 token by token (5.3 TB/s); 64 rows of
+// 8 heads 2.1 us.  Counters with kShort, head by head / token by token: 62 / 68 % of the issue slots, 58 / 62 %
+// of DRAM's rate, half of a warp's time waits for loads.  What stored head by head costs is its writes: a word
+// of scales is a sector of its own, 6.3 instead of 3.5 million sectors.
 #pragma once
 #include <cfloat>
 #include <cstdint>

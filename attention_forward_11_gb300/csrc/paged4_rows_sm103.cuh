@@ -27,13 +27,19 @@
 // free of bank conflicts.  L2 is asked for no more than a row of codes, since the next 64 bytes
 // belong to another head where pages are stored token by token (280 to 203 us).
 //
-// 144 sequences as above take 152 us, 4.8 TB/s of cache (203 stored token by token; the 16-bit
-// kernel 1.75 times as long on 48 of them); 8 of 32768 keys, one key head, 20 us (29 in 16 bits);
-// one of 1000 keys, 8 heads, 11 us (10), a block's start and end.  Bulk copies of 1 KB in place of
-// cp.async took 175 us, slices of 16 keys 189.
+// 144 sequences as above take 152 us, 4.8 TB/s of cache (48 of them 60, in 16 bits 134); the same heads of 64
+// 103 us; 8 of 32768 keys, one key head, 20 us (30 in 16 bits); one of 1000 keys, 8 heads, 11 us (10), a
+// block's start and end.  Stored token by token 144 take 204 us (heads of 64 213): a head's 64 or 32 bytes of codes
+// and 8 or 4 of scales lie apart from the next token's, and 1.15 GB are read for 0.73.  No unit is full at 152 us:
+// 2.6 instructions a cycle of 4, ALU pipe 55 %, DRAM 58 %; what a key costs whatever its head size (look-ups,
+// addresses, masks, maximum, exponentials) is a third of the time at 128 and half at 64.  Drafted tokens (16 x 5,
+// 4 heads of 64 a key head: 38 us, 6 of bytes) issue 1.1 instructions a cycle: a third of a warp's time waits for
+// instructions to be fetched, since three row blocks unrolled are more code than the cache nearest to the
+// schedulers holds, and eight warps hide little.  Bulk copies of 1 KB in place of cp.async took 175 us, slices of
+// 16 keys 189.
 //
 // P is rounded to fp16 for its product whatever q's type, which the products' operands are too:
-// against 64 bits O is off by 1.7e-3 of its norm in bf16 and 2.6e-4 in fp16, of which O's own rounding is
+// against 64 bits O is off by 1.7e-3 of its norm in bf16 and 2.5e-4 to 2.9e-4 in fp16, of which O's own rounding is
 // 1.65e-3 and 2.1e-4.
 #pragma once
 #include <cmath>

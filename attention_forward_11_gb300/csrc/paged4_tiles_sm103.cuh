@@ -17,9 +17,9 @@
 //     behind it: item j's epilogue runs after the fill of the stage behind the one with its last V.
 //     It stores O as it comes out of tensor memory, a row's 64 bytes a thread.
 //
-// 512 tokens on 32256 cached ones, 64/8 heads of 128, take 428 us, 1275 TFLOP/s (the 16-bit kernel 337);
-// at head size 64 286 (252); two prompts of 8192, 32/8 heads, 808 us (630); 4 chunks of 100 to 512 among 36
-// tokens 165 us (171).  What bounds it is the fills' warpgroup, 2750 busy cycles a step of two row
+// 512 tokens on 32256 cached ones, 64/8 heads of 128, take 418 us, 1300 TFLOP/s (the 16-bit kernel 336);
+// at head size 64 287 (254); two prompts of 8192, 32/8 heads, 788 us (629); 4 chunks of 100 to 512 among 36
+// tokens 166 us (172).  What bounds it is the fills' warpgroup, 2750 busy cycles a step of two row
 // tiles (1150 of conversions and stores, 1175 of page numbers, addresses and copies), and shared memory,
 // which the products read at its full rate half of the time.  Measured and not kept: codes by TMA into
 // shared staging (614 us); copies or addresses by other warps of the MMA's warpgroup, which slow its
@@ -58,13 +58,14 @@ struct Tiles4Geo {
     static_assert(kD == 64 || kD == 128, "head size 64 or 128");
     static constexpr int kTile = kBN;
     static constexpr int kRows = kTiles * kBM;
-    // 32 rows on 1000 keys, 8 heads: shares of at least 2 tiles 16.5 us, of 4 19.6 us; 8 sequences
-    // of 200 to 600 keys: units up to 8 tiles longer than a share whole 18.1 us, up to 2 21.1 us
+    // 32 rows on 1000 keys, 8 heads: shares of at least 2 tiles 18.4 us, of 4 21.0 us (256 rows 25.1 / 27.6);
+    // 8 sequences of 200 to 600 keys: units up to 8 tiles longer than a share whole 18.7 us, up to 2 20.0 us
+    // (14.8 / 17.0 at head size 64)
     static constexpr int kMinPiece = 2, kMinShare = 2, kCutTiles = 8;
     using ShareT = Share<kTile, kMinPiece, kMinShare>;
     using CursorT = Cursor<ShareT, kTile>;
     // K/V stages in flight, as many as fit beside Q: two of 64 KB at head size 128, four of
-    // 32 KB at 64 (where the softmax paces a step and two measured within 1 %).
+    // 32 KB at 64 (3 or 2 there are as fast: a chunk of 512 on 32256 285 us, two prompts of 8192 600).
     static constexpr int kStages = kD == 64 ? 4 : 2;
     static constexpr int kHalves = kD / 64;
     static constexpr int kTileBytes = kBM * kD * 2;  // Q, K or V tile
@@ -172,6 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_for_primary();
     typename T::ShareT sh;
     if (threadIdx.x == 0) sp.ws.header[blockIdx.x].n = 0;
+    // Units up to 1.35 shares whole at head size 128, as in the 16-bit kernel.  Codes need L2 less: 576 to 416
+    // tokens on 32000 keys, 64/8 heads, whole / cut 396 / 399, 400 / 379, 398 / 358, 396 / 336, 315 / 315, 295 / 294 us;
+    // on 8000 119 / 119, 118 / 124, 117 / 117, 118 / 111, 106 / 106, 99 / 99.
     if (!find_share<kThreads, typename T::ShareT, T::kTile, T::kMinShare, T::kCutTiles, kD == 128>(
             p, sp, reinterpret_cast<long long*>(smem + T::kSmemPart), start, sh)) {
         if (warp == 0) tmem_dealloc(tmem_base, kTmemCols);
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item wn;
         bool have_n = false;
         // Step kt of item j.  The last step of an item is code of its own and the tiles are
-        // unrolled: the loop over the others stays a straight run of MMAs (2900 to 2700
-        // cycles a step).
+        // unrolled: the loop over the others stays a straight run of MMAs, as in the 16-bit kernel,
+        // where that was measured.
         auto step = [&](auto last_step, int j, int kt) -> bool {
             constexpr bool kLast = decltype(last_step)::value;
             const int vs = kv % kStages;
