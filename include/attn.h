@@ -299,8 +299,10 @@ attn_status_t attn_paged_append(const void* k, const void* v, const long long* s
  * Arithmetic as attn_fwd: operands and P in the element type, products and softmax
  * statistics in fp32, O rounded to nearest even once.  Results do not depend on timing:
  * two calls with equal arguments give equal bits.  Asynchronous on `stream`; o, lse and
- * the workspace overlap no input and not each other.  On any error return nothing was
- * launched; a device-side timeout shows in attn_last_device_status.
+ * the workspace overlap no input and not each other.  On any error return that is not
+ * ATTN_ERR_CUDA nothing was launched; after that one, with up to three kernels in a call, o
+ * and lse are undefined (the call may be made again).  A device-side timeout shows in
+ * attn_last_device_status.
  */
 attn_status_t attn_paged_fwd_workspace_size(int total_q, int max_q_len, int Hq, int Hkv, int D, int page_size,
                                             size_t* bytes);
